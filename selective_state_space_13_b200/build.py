@@ -18,10 +18,18 @@ ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libss_b200.so")
 PROBE_LIB = os.path.join(PKG, "libss_probe.so")  # pipe-throughput probes of the benchmark
 PROBE_SOURCES = sorted(glob.glob(os.path.join(PKG, "csrc", "probe", "*.cu")))
+# the scan itself (the code that the recorded profiles of the scan belong to) ...
 SOURCES = sorted(glob.glob(os.path.join(PKG, "csrc", "*.cu")))
 HEADERS = sorted(glob.glob(os.path.join(PKG, "csrc", "*.h")) +
                  glob.glob(os.path.join(PKG, "csrc", "*.cuh")) +
-                 glob.glob(os.path.join(ROOT, "include", "*.h")))
+                 [os.path.join(ROOT, "include", "selective_scan.h")])
+# ... and the operators around it, in the same library
+OPS_SOURCES = sorted(glob.glob(os.path.join(PKG, "csrc", "ops", "*.cu")))
+OPS_HEADERS = sorted(glob.glob(os.path.join(PKG, "csrc", "ops", "*.h")) +
+                     glob.glob(os.path.join(PKG, "csrc", "ops", "*.cuh")) +
+                     [os.path.join(ROOT, "include", "selective_scan_ops.h")])
+LIB_SOURCES = SOURCES + OPS_SOURCES
+LIB_HEADERS = HEADERS + OPS_HEADERS
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
@@ -38,26 +46,26 @@ def stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(f) > t for f in SOURCES + HEADERS)
+    return any(os.path.getmtime(f) > t for f in LIB_SOURCES + LIB_HEADERS)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every csrc/*.cu to an object (in parallel), then link the shared library."""
+    """Compile every source of the library to an object (in parallel), then link it."""
     if not force and not stale():
         return LIB
     objdir = tempfile.mkdtemp(prefix="ss_build_")
     try:
         def compile_one(src):
             obj = os.path.join(objdir, os.path.basename(src) + ".o")
-            cmd = [_nvcc()] + NVCC_FLAGS + ["-I", os.path.join(ROOT, "include"), "-c", "-o", obj,
-                                            src]
+            cmd = [_nvcc()] + NVCC_FLAGS + ["-I", os.path.join(ROOT, "include"), "-I",
+                                            os.path.join(PKG, "csrc"), "-c", "-o", obj, src]
             res = subprocess.run(cmd, capture_output=True, text=True)
             if res.returncode != 0:
                 raise RuntimeError("nvcc failed on %s:\n%s%s" % (src, res.stdout, res.stderr))
             return obj, res.stderr
 
-        with ThreadPoolExecutor(max(1, min(len(SOURCES), os.cpu_count() or 1))) as ex:
-            results = list(ex.map(compile_one, SOURCES))
+        with ThreadPoolExecutor(max(1, min(len(LIB_SOURCES), os.cpu_count() or 1))) as ex:
+            results = list(ex.map(compile_one, LIB_SOURCES))
         if verbose:
             for _, log in results:
                 sys.stdout.write(log)

@@ -1,0 +1,97 @@
+// Launch parameters and launchers of the operators around the scan, shared by their host entry
+// points (so_api.cu) and their kernels.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "selective_scan_ops.h"
+
+namespace so {
+
+// ---------------------------------------------------------------- gated linear recurrence
+
+struct RecParams {
+    const void* x;         // [batch, L, D] io
+    const void* gate;      // [batch, L, D] io
+    const float* bias;     // [D] or null
+    const float* init;     // [batch, D] or null
+    const void* out_in;    // backward: the forward call's output
+    const void* dout;      // backward
+    const float* dlast;    // backward: [batch, D] or null
+    void* out;             // forward: [batch, L, D]; backward: dx
+    void* dgate;           // backward
+    float* last;           // forward: last state or null; backward: dinitial or null
+    float* dbias_part;     // backward: [batch * S, D] partial sums of ds, or null
+    float* dbias;          // backward: [D] or null
+    float2* carry;         // [batch, S, D] aggregates of the segments (S > 1)
+    int64_t batch, L, D, seg_len;
+    int32_t S;
+    int32_t form, complement, reverse;
+};
+
+cudaError_t launch_recurrence(const RecParams& p, int io_dtype, bool backward, cudaStream_t st);
+
+// ---------------------------------------------------------------- gradient of the scan
+
+struct BwdParams {
+    const void *u, *delta, *B, *C, *z, *dout;
+    const float *A, *Dskip, *bias, *init, *dlast;
+    ss_scan_grads g;
+    float* ckpt;      // local states at the start of every time tile (thread order)
+    float* cum;       // [K*batch, tiles of time, D] Delta summed from the segment start (S > 1)
+    float* seg_h;     // [K*batch, S, D, 16] end state of a segment scanned from zero
+    float* seg_p;     // the same shape: product of Abar over the segment
+    float* seg_g;     // the same shape: gradient that a zero-ended segment hands to the one before
+    float* dbc;       // [K*batch, channel tiles, L, 2, 16] partial sums of dB and dC
+    float* dpar;      // [K*batch*S, D, 18] partial sums of dA, dDskip, ddelta_bias
+    float* du_part;   // [K, batch, L, D] (several directions share u)
+    float* dz_part;   // [K, batch, L, D] (several directions with a gate)
+    int64_t batch, L, D, seg_len;
+    int32_t N, K, S;
+    int32_t dirs[SS_MAX_DIRS];
+    int32_t H, W;
+    int32_t softplus, u_per_dir, params_per_dir;
+};
+
+constexpr int kBwdTile = 8;       // steps of a time tile: one checkpoint each
+constexpr int kBwdChannels = 64;  // channels of a CTA
+
+// One translation unit per io type.
+cudaError_t launch_scan_bwd_f32(const BwdParams& p, cudaStream_t st);
+cudaError_t launch_scan_bwd_bf16(const BwdParams& p, cudaStream_t st);
+
+// ---------------------------------------------------------------- single-token step
+
+struct StepParams {
+    const void *u, *delta, *B, *C, *z;
+    const float *A, *Dskip, *bias, *conv_w, *conv_b;
+    float* state;
+    const int32_t* slots;
+    void* conv_state;
+    void* out;
+    int64_t batch, D, num_slots;
+    int32_t N, softplus, conv_width;
+};
+
+cudaError_t launch_step(const StepParams& p, int io_dtype, cudaStream_t st);
+
+// ---------------------------------------------------------------- parked states
+
+struct StateParams {
+    const float* state_in;  // store
+    float* state_out;       // load
+    uint8_t* codes;
+    float* scales;
+    const int32_t* src;     // slots of the source pool, or null
+    const int32_t* dst;     // slots of the destination pool, or null
+    int64_t src_slots, dst_slots;
+    int64_t rows, D;
+    int32_t N, bits;
+};
+
+cudaError_t launch_state(const StateParams& p, bool load, cudaStream_t st);
+
+}  // namespace so

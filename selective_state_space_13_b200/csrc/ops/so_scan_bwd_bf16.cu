@@ -1,0 +1,11 @@
+// Gradient of the selective scan for __nv_bfloat16 io.
+#include "so_scan_bwd_kernels.cuh"
+
+namespace so {
+
+cudaError_t launch_scan_bwd_bf16(const BwdParams& p, cudaStream_t st)
+{
+    return launch_bwd_io<__nv_bfloat16>(p, st);
+}
+
+}  // namespace so

@@ -79,7 +79,7 @@ _lib = None
 
 def _source_digest() -> str:
     h = hashlib.sha256()
-    for f in _build.SOURCES + _build.HEADERS:
+    for f in _build.LIB_SOURCES + _build.LIB_HEADERS:
         with open(f, "rb") as fh:
             h.update(os.path.basename(f).encode())
             h.update(fh.read())
