@@ -194,9 +194,10 @@ ss_status plan_bwd(const ss_shape* s, const ss_direction_map* dmap, const ss_lau
     pl->off_ckpt = take(R * ntiles * ctiles * so::kBwdChannels * 16);
     if (pl->split) {
         pl->off_cum = take(R * ntiles * D);
-        pl->off_h = take(R * pl->S * D * 16);
-        pl->off_p = take(R * pl->S * D * 16);
-        pl->off_g = take(R * pl->S * D * 16);
+        const size_t cells = R * pl->S * ctiles * so::kBwdChannels * 16;
+        pl->off_h = take(cells);
+        pl->off_p = take(cells);
+        pl->off_g = take(cells);
     }
     pl->off_dbc = take(R * ctiles * L * 32);
     pl->off_dpar = take(R * pl->S * D * 18);

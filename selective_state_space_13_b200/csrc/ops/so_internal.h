@@ -40,9 +40,9 @@ struct BwdParams {
     const void *u, *delta, *B, *C, *z, *dout;
     const float *A, *Dskip, *bias, *init, *dlast;
     ss_scan_grads g;
-    float* ckpt;      // local states at the start of every time tile (thread order)
-    float* cum;       // [K*batch, tiles of time, D] Delta summed from the segment start (S > 1)
-    float* seg_h;     // [K*batch, S, D, 16] end state of a segment scanned from zero
+    float* ckpt;      // states at the start of every slice, from the segment start (thread order)
+    float* cum;       // [K*batch, slices, D] Delta summed from the segment start (SPLIT)
+    float* seg_h;     // [K*batch, S, D padded, 16] end state of a segment scanned from zero
     float* seg_p;     // the same shape: product of Abar over the segment
     float* seg_g;     // the same shape: gradient that a zero-ended segment hands to the one before
     float* dbc;       // [K*batch, channel tiles, L, 2, 16] partial sums of dB and dC
@@ -56,7 +56,7 @@ struct BwdParams {
     int32_t softplus, u_per_dir, params_per_dir;
 };
 
-constexpr int kBwdTile = 8;       // steps of a time tile: one checkpoint each
+constexpr int kBwdTile = 4;       // steps of a slice: one checkpoint each
 constexpr int kBwdChannels = 64;  // channels of a CTA
 
 // One translation unit per io type.

@@ -1,15 +1,18 @@
 // Gradient of the selective scan.
 //
-// Two sweeps over time tiles of kBwdTile steps.  The summary sweep runs the recurrence forward and
-// stores the state at the start of every tile (a checkpoint); the gradient sweep walks the tiles
-// backwards, recomputes a tile's states from its checkpoint into registers and runs the reverse
-// recurrence over them.  Nothing of size batch x L x D x N crosses HBM except one state in eight.
+// Two sweeps over the sequence. The summary sweep runs the recurrence forward and stores the state
+// at the start of every slice of kT steps (a checkpoint); the gradient sweep walks the slices
+// backwards, recomputes a slice's states from its checkpoint into registers and runs the reverse
+// recurrence over them.  Nothing of size batch x L x D x N crosses HBM except one state in kT.
 //
-// A CTA of 4 warps owns 64 channels of one (direction, batch row, segment).  A thread owns 2
-// channels x 4 states: 4 lanes make a channel, so the sums over states (y, sum g B, sum g A h) and
-// the sums over channels (dB, dC) are both shorter than with one thread per channel, where every
-// step would add 32 values over 32 lanes.  Both kinds go through shared memory: a lane stores its
-// partial sums once, and the threads that finish a (step, channel) or a (step, state) add them up.
+// A CTA of 4 warps owns 64 channels of one (direction, batch row, segment), a warp 16 of them, a
+// thread 2 adjacent channels x 4 states: 4 lanes make a channel.  The two channels are the halves
+// of every packed f32x2 operation, so Delta, Delta u and dy come out of shared memory as pairs and
+// B and C as duplicated pairs, with no moves to build operands.  The sums over states (y, sum g B,
+// sum g A h) and over channels (dB, dC) go through shared memory that is private to the warp: a
+// lane stores its partial sums once, and the lane that finishes a (step, channel pair) or a
+// (step, 4 states) adds them up, which costs fewer instructions than a butterfly of shuffles.
+// Warps meet twice per tile of kTL steps: when its rows have landed and B and C are converted.
 //
 // Sequences are cut into S segments when there are too few CTAs.  The summary sweep then starts
 // every segment from zero and also returns, per channel and state, the product P of its decays
@@ -20,6 +23,9 @@
 //
 // dB, dC and the parameter gradients leave each CTA as fp32 partial sums that a last launch adds
 // in a fixed order.
+//
+// fp32 io takes the decays as Abar - 1 = expm1(Delta A) and updates h <- h + ((Abar - 1) h + w B):
+// a decay near one, rounded to fp32, would lose 2^-25 of the state every step.
 #pragma once
 
 #include <type_traits>
@@ -30,10 +36,18 @@ namespace so {
 
 namespace {
 
-constexpr int kT = kBwdTile;
-constexpr int kC = kBwdChannels;
-constexpr int kBwdThreads = 128;
-constexpr int kNP = 16;  // states, padded
+constexpr int kT = kBwdTile;      // steps of a slice
+constexpr int kTL = 2 * kT;       // steps of a tile: what is loaded and prepared together
+constexpr int kC = kBwdChannels;  // channels of a CTA
+constexpr int kWarps = 4;
+constexpr int kBwdThreads = 32 * kWarps;
+constexpr int kWC = kC / kWarps;  // channels of a warp
+constexpr int kNP = 16;           // states, padded
+// row pitch of raw tiles: the 4 steps x 8 channel pairs that a warp reads together lie in
+// different banks
+constexpr int kPitch = kC + 16;
+constexpr int kPartPitch = 4 * kWC + 8;  // likewise for the partial sums of a step
+static_assert(kT == 4 && kWC == 16, "lane = 4 * (channel pair) + (state group or step of a slice)");
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p)
 {
@@ -51,123 +65,155 @@ __device__ __forceinline__ void cp16(void* dst, const void* src, bool valid)
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Position visited at step t (the index map of the scan orders).
-__device__ __forceinline__ int64_t pos_of(int dir, int64_t L, int32_t H, int32_t W, int64_t t)
+__device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ float2 ex2_2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
+
+// exp(x) - 1, relative error about 1e-7.
+__device__ __forceinline__ float2 expm1_2(float2 x)
 {
-    if (dir == SS_DIR_FWD)
-        return t;
-    if (dir == SS_DIR_REV)
-        return L - 1 - t;
-    const uint32_t s = static_cast<uint32_t>(dir == SS_DIR_COL_REV ? L - 1 - t : t);
-    const uint32_t col = s / static_cast<uint32_t>(H);
-    return static_cast<int64_t>(s - col * H) * W + col;
+    return make_float2(-one_minus_exp(x.x, ex2(x.x * kLog2e)), -one_minus_exp(x.y, ex2(x.y * kLog2e)));
 }
 
+// What a CTA works on.  Element offsets inside one sequence fit in 32 bits (L * D < 2^31).
 struct Unit {
-    int64_t kb, b, ub, c0, t0, t1, tile0;
-    int64_t ctile, ctiles, ntiles;
-    int k, seg, dir, cv;
+    int64_t kb, b, ub;           // row blocks of delta/B/C, of dout/z, of u
+    int c0, cv, ctile, ctiles;   // first channel, valid channels, channel tile
+    int t0, t1, L, D;            // steps of the segment
+    int k, seg, dir, H, W;
+
+    // Element offset of the row that step t visits.
+    __device__ __forceinline__ uint32_t row(int t) const
+    {
+        uint32_t pos = static_cast<uint32_t>(dir == SS_DIR_REV || dir == SS_DIR_COL_REV ? L - 1 - t : t);
+        if (dir == SS_DIR_COL || dir == SS_DIR_COL_REV) {
+            const uint32_t col = pos / static_cast<uint32_t>(H);
+            pos = (pos - col * H) * W + col;
+        }
+        return pos * static_cast<uint32_t>(D);
+    }
 };
 
 __device__ __forceinline__ Unit unit_of(const BwdParams& p)
 {
     Unit u;
-    int64_t i = blockIdx.x;
-    u.ctiles = (p.D + kC - 1) / kC;
+    u.D = static_cast<int>(p.D);
+    u.L = static_cast<int>(p.L);
+    u.ctiles = (u.D + kC - 1) / kC;
+    unsigned i = blockIdx.x;
     u.ctile = i % u.ctiles;
     i /= u.ctiles;
-    u.kb = i % (p.batch * p.K);
-    u.seg = static_cast<int>(i / (p.batch * p.K));
-    u.k = static_cast<int>(u.kb / p.batch);
+    const unsigned rows = static_cast<unsigned>(p.batch * p.K);
+    u.seg = i / rows;
+    const unsigned kb = i % rows;
+    u.k = kb / static_cast<unsigned>(p.batch);
+    u.kb = kb;
     u.b = u.kb - u.k * p.batch;
     u.ub = p.u_per_dir ? u.kb : u.b;
     u.dir = u.k == 0 ? p.dirs[0] : u.k == 1 ? p.dirs[1] : u.k == 2 ? p.dirs[2] : p.dirs[3];
+    u.H = p.H;
+    u.W = p.W;
     u.c0 = u.ctile * kC;
-    u.cv = static_cast<int>(p.D - u.c0 < kC ? p.D - u.c0 : kC);
-    u.t0 = u.seg * p.seg_len;
-    u.t1 = u.t0 + p.seg_len < p.L ? u.t0 + p.seg_len : p.L;
-    u.tile0 = u.t0 / kT;
-    u.ntiles = (p.L + kT - 1) / kT;
+    u.cv = min(u.D - u.c0, kC);
+    u.t0 = static_cast<int>(u.seg * p.seg_len);
+    u.t1 = static_cast<int>(min(p.L, u.seg * p.seg_len + p.seg_len));
     return u;
 }
 
-// One stage: the raw rows of a tile, and (gradient sweep) its checkpoint.
 template <typename io_t> struct Stage {
-    io_t u[kT][kC], delta[kT][kC], dout[kT][kC], z[kT][kC];
-    float4 ckpt[2][kBwdThreads];
+    io_t u[kTL][kPitch], delta[kTL][kPitch], dout[kTL][kPitch], z[kTL][kPitch];
 };
 
 template <typename io_t> struct SumSmem {
     Stage<io_t> st[2];
-    float4 scal[kT][kC];    // Delta, Delta u, dy
-    float B[kT][kNP], C[kT][kNP];
+    float2 B[kTL][kNP], C[kTL][kNP];       // duplicated
+    float2 scal[kWarps][kTL][3][kWC / 2];  // Delta, Delta u, dy of a channel pair
 };
 
 template <typename io_t> struct GradSmem {
     Stage<io_t> st[2];
-    float4 scal[kT][kC];
-    float B[kT][kNP], C[kT][kNP];
-    float part[3][kT][kC][4];               // y, sum g B, sum g A2 Abar h: one value per state group
-    float dbc[kT][2][kBwdThreads / 4][kNP];  // dB, dC of every (warp, channel group)
+    float2 B[kTL][kNP], C[kTL][kNP];
+    float2 scal[kWarps][kTL][3][kWC / 2];
+    float part[kWarps][3][kT][kPartPitch];  // y, sum g B, sum g A Abar h: [state group][channel]
+    float dbc[kWarps][kT][2][kWC / 2][kNP]; // dB, dC of every channel pair
+    float4 acc[kTL][2][kWarps][kNP / 4];    // dB, dC of every warp
 };
 
-// Starts the copies of time tile `tile` (steps t..t+rows-1) into a stage; returns the raw B and C
-// elements this thread will convert.
-template <typename io_t, bool GRAD>
-__device__ __forceinline__ void issue(const BwdParams& p, const Unit& un, int64_t tile,
-                                      Stage<io_t>& st, bool want_dy, io_t* bc)
+// Starts the copies of the tile of steps t..t+kTL-1 into a stage; returns the raw B and C elements
+// that this thread will convert.
+constexpr int kBC = kTL * kNP / kBwdThreads;
+static_assert(kBC * kBwdThreads == kTL * kNP, "whole rounds of B and C elements");
+
+template <typename io_t>
+__device__ __forceinline__ void issue(const BwdParams& p, const Unit& un, int t, Stage<io_t>& st,
+                                      bool want_dy, io_t (*bc)[2])
 {
     constexpr int E = 16 / sizeof(io_t);  // elements of a 16-byte piece
     constexpr int PR = kC / E;            // pieces of a row
-    const int64_t t = tile * kT;
-    const int rows = static_cast<int>(un.t1 - t < kT ? un.t1 - t : kT);
-    const io_t* gu = static_cast<const io_t*>(p.u) + un.ub * p.L * p.D + un.c0;
-    const io_t* gl = static_cast<const io_t*>(p.delta) + un.kb * p.L * p.D + un.c0;
-    const io_t* go = static_cast<const io_t*>(p.dout) + un.b * p.L * p.D + un.c0;
-    const io_t* gz = static_cast<const io_t*>(p.z);
+    const int rows = min(un.t1 - t, kTL);
+    const int64_t LD = p.L * p.D;
+    const io_t* gu = static_cast<const io_t*>(p.u) + un.ub * LD + un.c0;
+    const io_t* gl = static_cast<const io_t*>(p.delta) + un.kb * LD + un.c0;
+    const io_t* go = static_cast<const io_t*>(p.dout) + un.b * LD + un.c0;
+    const io_t* gz = p.z ? static_cast<const io_t*>(p.z) + un.b * LD + un.c0 : nullptr;
 #pragma unroll
-    for (int i = 0; i < kT * PR / kBwdThreads + (kT * PR % kBwdThreads ? 1 : 0); ++i) {
+    for (int i = 0; i < (kTL * PR + kBwdThreads - 1) / kBwdThreads; ++i) {
         const int j = threadIdx.x + i * kBwdThreads;
-        const int r = j / PR, c = (j % PR) * E;
-        if (j < kT * PR) {
+        if (j < kTL * PR) {
+            const int r = j / PR, c = (j % PR) * E;
             const bool ok = r < rows && c < un.cv;
-            const int64_t at = ok ? pos_of(un.dir, p.L, p.H, p.W, t + r) * p.D + c : 0;
+            const uint32_t at = ok ? un.row(t + r) + c : 0;
             cp16(&st.u[r][c], gu + at, ok);
-            cp16(&st.delta[r][c], gl + (ok ? (t + r) * p.D + c : 0), ok);
+            cp16(&st.delta[r][c], gl + (ok ? static_cast<uint32_t>(t + r) * un.D + c : 0u), ok);
             if (want_dy) {
                 cp16(&st.dout[r][c], go + at, ok);
                 if (gz)
-                    cp16(&st.z[r][c], gz + un.b * p.L * p.D + un.c0 + at, ok);
+                    cp16(&st.z[r][c], gz + at, ok);
             }
         }
     }
-    if (GRAD) {
-        const float4* ck = reinterpret_cast<const float4*>(p.ckpt) +
-                           ((un.kb * un.ntiles + tile) * un.ctiles + un.ctile) * 2 * kBwdThreads;
-        cp16(&st.ckpt[0][threadIdx.x], ck + threadIdx.x, true);
-        cp16(&st.ckpt[1][threadIdx.x], ck + kBwdThreads + threadIdx.x, true);
-    }
     cp_commit();
-    const int r = threadIdx.x / kNP, n = threadIdx.x % kNP;
-    static_assert(kT * kNP == kBwdThreads, "one B and one C element a thread");
-    const bool ok = r < rows && n < p.N;
-    const int64_t at = (un.kb * p.L + t + r) * p.N + n;
-    bc[0] = ok ? static_cast<const io_t*>(p.B)[at] : io_t(0.f);
-    bc[1] = ok ? static_cast<const io_t*>(p.C)[at] : io_t(0.f);
+    const io_t* gB = static_cast<const io_t*>(p.B) + (un.kb * p.L + t) * p.N;
+    const io_t* gC = static_cast<const io_t*>(p.C) + (un.kb * p.L + t) * p.N;
+#pragma unroll
+    for (int i = 0; i < kBC; ++i) {
+        const int j = threadIdx.x + i * kBwdThreads, r = j / kNP, n = j % kNP;
+        const bool ok = r < rows && n < p.N;
+        bc[i][0] = ok ? gB[r * p.N + n] : io_t(0.f);
+        bc[i][1] = ok ? gC[r * p.N + n] : io_t(0.f);
+    }
 }
 
-// Per-channel parameters of the two channels whose elementwise work a thread does.
+// The thread's place: channels c, c+1 of the CTA, states 4 ng .. 4 ng + 3; in elementwise work,
+// the channel pair's step ng of a slice.
+struct Cell {
+    int warp, lane, cg, ng, c;
+    bool valid;  // the channels exist (they come in pairs: D is a multiple of 4)
+};
+
+__device__ __forceinline__ Cell cell_of(const Unit& un)
+{
+    Cell x;
+    x.lane = threadIdx.x & 31;
+    x.warp = threadIdx.x >> 5;
+    x.cg = x.lane >> 2;
+    x.ng = x.lane & 3;
+    x.c = x.warp * kWC + 2 * x.cg;
+    x.valid = x.c < un.cv;
+    return x;
+}
+
+// Per-channel parameters of the thread's channel pair.
 struct Par {
     float2 skip, bias;
 };
 
-__device__ __forceinline__ Par load_par(const BwdParams& p, const Unit& un)
+__device__ __forceinline__ Par load_par(const BwdParams& p, const Unit& un, const Cell& x)
 {
-    const int c = 2 * (threadIdx.x & 31);
-    const int64_t d = (p.params_per_dir ? un.k * p.D : 0) + un.c0 + c;
+    const int64_t d = (p.params_per_dir ? un.k * p.D : 0) + un.c0 + x.c;
     Par q;
-    q.skip = q.bias = make_float2(0.f, 0.f);
-    if (c < un.cv) {
+    q.skip = q.bias = dup(0.f);
+    if (x.valid) {
         if (p.Dskip)
             q.skip = make_float2(p.Dskip[d], p.Dskip[d + 1]);
         if (p.bias)
@@ -176,93 +222,149 @@ __device__ __forceinline__ Par load_par(const BwdParams& p, const Unit& un)
     return q;
 }
 
-template <typename io_t> __device__ __forceinline__ float2 pair_at(const io_t* row, int c)
+// A of the thread's cells, times log2(e) for the exponentials in base 2 (not for fp32 io, which
+// takes expm1).
+template <bool PRECISE>
+__device__ __forceinline__ void load_A(const BwdParams& p, const Unit& un, const Cell& x, float2 A[4])
 {
-    return Pair<io_t>::f(*reinterpret_cast<const typename Pair<io_t>::raw*>(row + c));
+    const int64_t d = (p.params_per_dir ? un.k * p.D : 0) + un.c0 + x.c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int n = 4 * x.ng + i;
+        A[i] = dup(0.f);
+        if (x.valid && n < p.N)
+            A[i] = make_float2(p.A[d * p.N + n], p.A[(d + 1) * p.N + n]);
+        if (!PRECISE)
+            A[i] = __fmul2_rn(A[i], dup(kLog2e));
+    }
 }
 
-// Delta, Delta u and dy of the tile, two channels and every fourth step a thread; steps behind
-// the segment and channels behind the row become Delta = 0 (a step that changes nothing).
-template <typename io_t, typename Smem>
-__device__ __forceinline__ void prepass(const BwdParams& p, const Unit& un, int64_t tile, Smem& sm,
-                                        const Stage<io_t>& st, const Par& par, bool want_dy,
-                                        const io_t* bc)
+// The decay of a step: Abar, or Abar - 1 with PRECISE.
+template <bool PRECISE> __device__ __forceinline__ float2 decay(float2 delta, float2 A)
 {
-    const int c = 2 * (threadIdx.x & 31);
-    const int rows = static_cast<int>(un.t1 - tile * kT < kT ? un.t1 - tile * kT : kT);
+    const float2 x = __fmul2_rn(delta, A);
+    return PRECISE ? expm1_2(x) : ex2_2(x);
+}
+
+// Abar v + w with that decay.
+template <bool PRECISE> __device__ __forceinline__ float2 decayed(float2 a, float2 v, float2 w)
+{
+    return PRECISE ? __fadd2_rn(v, __ffma2_rn(a, v, w)) : __ffma2_rn(a, v, w);
+}
+
+template <bool PRECISE> __device__ __forceinline__ float2 decayed(float2 a, float2 v)
+{
+    return PRECISE ? __ffma2_rn(a, v, v) : __fmul2_rn(a, v);
+}
+
+template <typename io_t> __device__ __forceinline__ float2 pair_at(const io_t* p)
+{
+    return Pair<io_t>::f(*reinterpret_cast<const typename Pair<io_t>::raw*>(p));
+}
+
+__device__ __forceinline__ float2 sigmoid_2(float2 x)
+{
+    return make_float2(sigmoid_f(x.x), sigmoid_f(x.y));
+}
+
+// softplus of a pair (softplus_f, its polynomial in packed operations).
+__device__ __forceinline__ float2 softplus_2(float2 x)
+{
+    const float2 e = ex2_2(__fmul2_rn(make_float2(-fabsf(x.x), -fabsf(x.y)), dup(kLog2e)));
+    const float2 s = __fmul2_rn(e, make_float2(rcp(2.f + e.x), rcp(2.f + e.y)));
+    const float2 s2 = __fmul2_rn(s, s);
+    float2 q = __ffma2_rn(dup(2.f / 15.f), s2, dup(2.f / 13.f));
+    q = __ffma2_rn(q, s2, dup(2.f / 11.f));
+    q = __ffma2_rn(q, s2, dup(2.f / 9.f));
+    q = __ffma2_rn(q, s2, dup(2.f / 7.f));
+    q = __ffma2_rn(q, s2, dup(2.f / 5.f));
+    q = __ffma2_rn(q, s2, dup(2.f / 3.f));
+    q = __ffma2_rn(q, s2, dup(2.f));
+    return __ffma2_rn(s, q, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
+}
+
+// Delta, Delta u and dy of the tile for the warp's channels, and B and C for the CTA.  Steps behind
+// the segment and channels behind the row become Delta = 0, a step that changes nothing.
+template <typename io_t, typename Smem>
+__device__ __forceinline__ void prepass(const BwdParams& p, const Unit& un, const Cell& x, int t,
+                                        Smem& sm, const Stage<io_t>& st, const Par& par,
+                                        bool want_dy, const io_t (*bc)[2])
+{
+    const int rows = min(un.t1 - t, kTL);
 #pragma unroll
-    for (int r = threadIdx.x >> 5; r < kT; r += kBwdThreads / 32) {
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-        if (r < rows && c < un.cv) {
-            const float2 u = pair_at(st.u[r], c), l = pair_at(st.delta[r], c);
-            a.x = l.x + par.bias.x;
-            b.x = l.y + par.bias.y;
-            if (p.softplus) {
-                a.x = softplus_f(a.x);
-                b.x = softplus_f(b.x);
-            }
-            a.y = a.x * u.x;
-            b.y = b.x * u.y;
+    for (int r = x.ng; r < kTL; r += kT) {
+        float2 dl = dup(0.f), w = dl, dy = dl;
+        if (r < rows && x.valid) {
+            dl = __fadd2_rn(pair_at(&st.delta[r][x.c]), par.bias);
+            if (p.softplus)
+                dl = softplus_2(dl);
+            w = __fmul2_rn(dl, pair_at(&st.u[r][x.c]));
             if (want_dy) {
-                const float2 o = pair_at(st.dout[r], c);
-                a.z = o.x;
-                b.z = o.y;
+                dy = pair_at(&st.dout[r][x.c]);
                 if (p.z) {
-                    const float2 z = pair_at(st.z[r], c);
-                    a.z *= silu_f(z.x);
-                    b.z *= silu_f(z.y);
+                    const float2 z = pair_at(&st.z[r][x.c]);
+                    dy = __fmul2_rn(dy, __fmul2_rn(z, sigmoid_2(z)));
                 }
             }
         }
-        sm.scal[r][c] = a;
-        sm.scal[r][c + 1] = b;
+        sm.scal[x.warp][r][0][x.cg] = dl;
+        sm.scal[x.warp][r][1][x.cg] = w;
+        if (want_dy)
+            sm.scal[x.warp][r][2][x.cg] = dy;
     }
-    const int r = threadIdx.x / kNP, n = threadIdx.x % kNP;
-    sm.B[r][n] = ld1(&bc[0]);
-    sm.C[r][n] = ld1(&bc[1]);
-}
-
-// The thread's 2 channels x 4 states.
-struct Cell {
-    int ng, c[2];
-};
-
-__device__ __forceinline__ Cell cell_of()
-{
-    Cell x;
-    const int lane = threadIdx.x & 31;
-    x.ng = lane & 3;
-    x.c[0] = (threadIdx.x >> 5) * 16 + (lane >> 2);
-    x.c[1] = x.c[0] + 8;
-    return x;
-}
-
-__device__ __forceinline__ void load_A2(const BwdParams& p, const Unit& un, const Cell& x,
-                                        float2 A2[2][2])
-{
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        float a[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = 4 * x.ng + i;
-            const int64_t d = (p.params_per_dir ? un.k * p.D : 0) + un.c0 + x.c[j];
-            a[i] = x.c[j] < un.cv && n < p.N ? p.A[d * p.N + n] * kLog2e : 0.f;
-        }
-        A2[j][0] = make_float2(a[0], a[1]);
-        A2[j][1] = make_float2(a[2], a[3]);
+    for (int i = 0; i < kBC; ++i) {
+        const int j = threadIdx.x + i * kBwdThreads;
+        sm.B[j / kNP][j % kNP] = dup(ld1(&bc[i][0]));
+        sm.C[j / kNP][j % kNP] = dup(ld1(&bc[i][1]));
     }
 }
 
-__device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
-
-__device__ __forceinline__ float2 ex2_2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
-
-// Index of this thread's states in [K*batch, S, D, 16] arrays (channel j).
-__device__ __forceinline__ int64_t seg_at(const BwdParams& p, const Unit& un, const Cell& x, int seg,
-                                          int j)
+// The thread's 4 duplicated elements of a row of B or C.
+__device__ __forceinline__ void load4(const float2 (*rows)[kNP], int r, int ng, float2 v[4])
 {
-    return ((un.kb * p.S + seg) * p.D + un.c0 + x.c[j]) * kNP + 4 * x.ng;
+    const float4 a = *reinterpret_cast<const float4*>(&rows[r][4 * ng]);
+    const float4 b = *reinterpret_cast<const float4*>(&rows[r][4 * ng + 2]);
+    v[0] = make_float2(a.x, a.y);
+    v[1] = make_float2(a.z, a.w);
+    v[2] = make_float2(b.x, b.y);
+    v[3] = make_float2(b.z, b.w);
+}
+
+// Per-thread arrays in global memory as two float4 per cell block.
+__device__ __forceinline__ void put4(float4* at, int stride, const float2 v[4])
+{
+    at[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    at[stride] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+}
+
+__device__ __forceinline__ void get4(const float4* at, int stride, float2 v[4])
+{
+    const float4 a = at[0], b = at[stride];
+    v[0] = make_float2(a.x, a.y);
+    v[1] = make_float2(a.z, a.w);
+    v[2] = make_float2(b.x, b.y);
+    v[3] = make_float2(b.z, b.w);
+}
+
+// Checkpoint of this thread for slice `s` of the sequence, and the block of a segment.
+__device__ __forceinline__ float4* ckpt_at(const BwdParams& p, const Unit& un, int s)
+{
+    const int64_t nslices = (p.L + kT - 1) / kT;
+    return reinterpret_cast<float4*>(p.ckpt) +
+           ((un.kb * nslices + s) * un.ctiles + un.ctile) * (2 * kBwdThreads) + threadIdx.x;
+}
+
+__device__ __forceinline__ float4* seg_at(float* base, const BwdParams& p, const Unit& un, int seg)
+{
+    return reinterpret_cast<float4*>(base) +
+           ((un.kb * p.S + seg) * un.ctiles + un.ctile) * (2 * kBwdThreads) + threadIdx.x;
+}
+
+__device__ __forceinline__ float2* cum_at(const BwdParams& p, const Unit& un, const Cell& x, int s)
+{
+    const int64_t nslices = (p.L + kT - 1) / kT;
+    return reinterpret_cast<float2*>(p.cum + (un.kb * nslices + s) * p.D + un.c0 + x.c);
 }
 
 // ------------------------------------------------------------------------- summary sweep
@@ -270,335 +372,320 @@ __device__ __forceinline__ int64_t seg_at(const BwdParams& p, const Unit& un, co
 template <typename io_t, bool SPLIT>
 __global__ void __launch_bounds__(kBwdThreads) summary_kernel(const __grid_constant__ BwdParams p)
 {
+    constexpr bool PRECISE = std::is_same<io_t, float>::value;
     extern __shared__ __align__(128) unsigned char raw_smem[];
     SumSmem<io_t>& sm = *reinterpret_cast<SumSmem<io_t>*>(raw_smem);
     const Unit un = unit_of(p);
-    const Cell x = cell_of();
-    const Par par = load_par(p, un);
-    float2 A2[2][2], h[2][2], P[2][2], G[2][2];
-    load_A2(p, un, x, A2);
-    float cum[2] = {0.f, 0.f};
+    const Cell x = cell_of(un);
+    const Par par = load_par(p, un, x);
+    float2 A[4], h[4], P[4], G[4], cum = dup(0.f);
+    load_A<PRECISE>(p, un, x, A);
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            h[j][i] = G[j][i] = dup(0.f);
-            P[j][i] = dup(1.f);
-        }
-    const int64_t ntile = (un.t1 - un.t0 + kT - 1) / kT;
-    io_t bc[2];
-    issue<io_t, false>(p, un, un.tile0, sm.st[0], SPLIT, bc);
-    for (int64_t it = 0; it < ntile; ++it) {
-        const int64_t tile = un.tile0 + it;
+    for (int i = 0; i < 4; ++i) {
+        h[i] = G[i] = dup(0.f);
+        P[i] = dup(1.f);
+    }
+    io_t bc[kBC][2];
+    issue<io_t>(p, un, un.t0, sm.st[0], SPLIT, bc);
+    for (int t = un.t0, it = 0; t < un.t1; t += kTL, ++it) {
         cp_wait_all();
         __syncthreads();
-        prepass(p, un, tile, sm, sm.st[it & 1], par, SPLIT, bc);
+        prepass(p, un, x, t, sm, sm.st[it & 1], par, SPLIT, bc);
         __syncthreads();
-        if (it + 1 < ntile)
-            issue<io_t, false>(p, un, tile + 1, sm.st[(it + 1) & 1], SPLIT, bc);
-        float4* ck = reinterpret_cast<float4*>(p.ckpt) +
-                     ((un.kb * un.ntiles + tile) * un.ctiles + un.ctile) * 2 * kBwdThreads;
+        if (t + kTL < un.t1)
+            issue<io_t>(p, un, t + kTL, sm.st[(it + 1) & 1], SPLIT, bc);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            ck[j * kBwdThreads + threadIdx.x] =
-                make_float4(h[j][0].x, h[j][0].y, h[j][1].x, h[j][1].y);
-            if (SPLIT && x.ng == 0 && x.c[j] < un.cv)
-                p.cum[(un.kb * un.ntiles + tile) * p.D + un.c0 + x.c[j]] = cum[j];
-        }
+        for (int r = 0; r < kTL; ++r) {
+            if (r % kT == 0 && t + r < un.t1) {
+                put4(ckpt_at(p, un, (t + r) / kT), kBwdThreads, h);
+                if (SPLIT && x.ng == 0 && x.valid)
+                    *cum_at(p, un, x, (t + r) / kT) = cum;
+            }
+            float2 B[4], C[4];
+            load4(sm.B, r, x.ng, B);
+            const float2 dl = sm.scal[x.warp][r][0][x.cg], w = sm.scal[x.warp][r][1][x.cg];
+            float2 dy = dup(0.f);
+            if (SPLIT) {
+                load4(sm.C, r, x.ng, C);
+                dy = sm.scal[x.warp][r][2][x.cg];
+                cum = __fadd2_rn(cum, dl);
+            }
 #pragma unroll
-        for (int r = 0; r < kT; ++r) {
-            const float4 B4 = *reinterpret_cast<const float4*>(&sm.B[r][4 * x.ng]);
-            const float2 B[2] = {make_float2(B4.x, B4.y), make_float2(B4.z, B4.w)};
-            const float4 C4 = *reinterpret_cast<const float4*>(&sm.C[r][4 * x.ng]);
-            const float2 C[2] = {make_float2(C4.x, C4.y), make_float2(C4.z, C4.w)};
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float4 s = sm.scal[r][x.c[j]];
-                if (SPLIT)
-                    cum[j] += s.x;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float2 a = ex2_2(__fmul2_rn(dup(s.x), A2[j][i]));
-                    h[j][i] = __ffma2_rn(a, h[j][i], __fmul2_rn(dup(s.y), B[i]));
-                    if (SPLIT) {
-                        P[j][i] = __fmul2_rn(P[j][i], a);
-                        G[j][i] = __ffma2_rn(P[j][i], __fmul2_rn(dup(s.z), C[i]), G[j][i]);
-                    }
+            for (int i = 0; i < 4; ++i) {
+                const float2 a = decay<PRECISE>(dl, A[i]);
+                h[i] = decayed<PRECISE>(a, h[i], __fmul2_rn(w, B[i]));
+                if (SPLIT) {
+                    P[i] = decayed<PRECISE>(a, P[i]);
+                    G[i] = __ffma2_rn(P[i], __fmul2_rn(dy, C[i]), G[i]);
                 }
             }
         }
     }
     if (SPLIT) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            if (x.c[j] < un.cv) {
-                const int64_t at = seg_at(p, un, x, un.seg, j);
-                *reinterpret_cast<float4*>(p.seg_h + at) =
-                    make_float4(h[j][0].x, h[j][0].y, h[j][1].x, h[j][1].y);
-                *reinterpret_cast<float4*>(p.seg_p + at) =
-                    make_float4(P[j][0].x, P[j][0].y, P[j][1].x, P[j][1].y);
-                *reinterpret_cast<float4*>(p.seg_g + at) =
-                    make_float4(G[j][0].x, G[j][0].y, G[j][1].x, G[j][1].y);
-            }
+        put4(seg_at(p.seg_h, p, un, un.seg), kBwdThreads, h);
+        put4(seg_at(p.seg_p, p, un, un.seg), kBwdThreads, P);
+        put4(seg_at(p.seg_g, p, un, un.seg), kBwdThreads, G);
     }
 }
 
 // ------------------------------------------------------------------------- gradient sweep
 
-// The elementwise end of a tile, two channels and every fourth step a thread, and the sums of its
-// dB and dC over the CTA's channels.
+// The elementwise end of a slice (steps t..t+kT-1, rows r0.. of the stage): a lane has one step of
+// its channel pair; and the warp's sums of dB and dC.
 template <typename io_t>
-__device__ __forceinline__ void finish_tile(const BwdParams& p, const Unit& un, int64_t tile,
-                                            GradSmem<io_t>& sm, const Stage<io_t>& st, const Par& par,
-                                            float2& dskip, float2& dbias)
+__device__ __forceinline__ void finish_slice(const BwdParams& p, const Unit& un, const Cell& x, int t,
+                                             int r0, GradSmem<io_t>& sm, const Stage<io_t>& st,
+                                             const Par& par, float2& dskip, float2& dbias)
 {
     using P2 = Pair<io_t>;
     using raw = typename P2::raw;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = 2 * lane;
-    const int64_t t = tile * kT;
-    const int rows = static_cast<int>(un.t1 - t < kT ? un.t1 - t : kT);
-#pragma unroll
-    for (int r = warp; r < kT; r += kBwdThreads / 32)
-        if (r < rows && c < un.cv) {
-            float du[2], dl[2], dz[2];
-            const float2 u2 = pair_at(st.u[r], c), l2 = pair_at(st.delta[r], c);
-            const float2 o2 = pair_at(st.dout[r], c);
-            const float2 z2 = p.z ? pair_at(st.z[r], c) : make_float2(0.f, 0.f);
-            const float u[2] = {u2.x, u2.y}, o[2] = {o2.x, o2.y}, z[2] = {z2.x, z2.y};
-            const float l[2] = {l2.x + par.bias.x, l2.y + par.bias.y};
-            const float skip[2] = {par.skip.x, par.skip.y};
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float4 s = sm.scal[r][c + j];
-                const float4 b4 = *reinterpret_cast<const float4*>(sm.part[1][r][c + j]);
-                const float4 a4 = *reinterpret_cast<const float4*>(sm.part[2][r][c + j]);
-                const float gB = (b4.x + b4.y) + (b4.z + b4.w);
-                const float gA = ((a4.x + a4.y) + (a4.z + a4.w)) * kLn2;
-                du[j] = fmaf(skip[j], s.z, s.x * gB);
-                dl[j] = fmaf(u[j], gB, gA);
-                if (p.softplus)
-                    dl[j] *= sigmoid_f(l[j]);
-                if (p.z) {
-                    const float4 y4 = *reinterpret_cast<const float4*>(sm.part[0][r][c + j]);
-                    const float y = fmaf(skip[j], u[j], (y4.x + y4.y) + (y4.z + y4.w));
-                    const float sg = sigmoid_f(z[j]);
-                    dz[j] = o[j] * y * sg * fmaf(z[j], 1.f - sg, 1.f);
-                }
-            }
-            const float4 s0 = sm.scal[r][c], s1 = sm.scal[r][c + 1];
-            dskip.x = fmaf(s0.z, u[0], dskip.x);
-            dskip.y = fmaf(s1.z, u[1], dskip.y);
-            dbias.x += dl[0];
-            dbias.y += dl[1];
-            const int64_t at = pos_of(un.dir, p.L, p.H, p.W, t + r) * p.D + un.c0 + c;
-            if (p.du_part)
-                *reinterpret_cast<float2*>(p.du_part + un.kb * p.L * p.D + at) =
-                    make_float2(du[0], du[1]);
+    constexpr bool PRECISE = std::is_same<io_t, float>::value;
+    const int r = r0 + x.ng;
+    if (t + x.ng < un.t1 && x.valid) {
+        const float2 dl = sm.scal[x.warp][r][0][x.cg], dy = sm.scal[x.warp][r][2][x.cg];
+        const float2 u = pair_at(&st.u[r][x.c]);
+        auto sum = [&](int q) {
+            const float* s = &sm.part[x.warp][q][x.ng][2 * x.cg];
+            const float2 a = *reinterpret_cast<const float2*>(s);
+            const float2 b = *reinterpret_cast<const float2*>(s + kWC);
+            const float2 c = *reinterpret_cast<const float2*>(s + 2 * kWC);
+            const float2 d = *reinterpret_cast<const float2*>(s + 3 * kWC);
+            return __fadd2_rn(__fadd2_rn(a, b), __fadd2_rn(c, d));
+        };
+        const float2 gB = sum(1);
+        float2 gA = sum(2);
+        if (!PRECISE)
+            gA = __fmul2_rn(gA, dup(kLn2));  // A was in base 2
+        const float2 du = __ffma2_rn(par.skip, dy, __fmul2_rn(dl, gB));
+        float2 dd = __ffma2_rn(u, gB, gA);
+        if (p.softplus)
+            dd = __fmul2_rn(dd, sigmoid_2(__fadd2_rn(pair_at(&st.delta[r][x.c]), par.bias)));
+        dskip = __ffma2_rn(dy, u, dskip);
+        dbias = __fadd2_rn(dbias, dd);
+        const uint32_t at = un.row(t + x.ng) + un.c0 + x.c;
+        const int64_t LD = p.L * p.D;
+        if (p.du_part)
+            *reinterpret_cast<float2*>(p.du_part + un.kb * LD + at) = du;
+        else
+            *reinterpret_cast<raw*>(static_cast<io_t*>(p.g.du) + un.ub * LD + at) = P2::r(du);
+        *reinterpret_cast<raw*>(static_cast<io_t*>(p.g.ddelta) + un.kb * LD +
+                                (static_cast<uint32_t>(t + x.ng) * un.D + un.c0 + x.c)) = P2::r(dd);
+        if (p.z) {
+            const float2 z = pair_at(&st.z[r][x.c]), sg = sigmoid_2(z);
+            const float2 y = __ffma2_rn(par.skip, u, sum(0));
+            // silu'(z) = sg (1 + z (1 - sg))
+            const float2 one = dup(1.f), rest = make_float2(1.f - sg.x, 1.f - sg.y);
+            const float2 dz = __fmul2_rn(__fmul2_rn(pair_at(&st.dout[r][x.c]), y),
+                                         __fmul2_rn(sg, __ffma2_rn(z, rest, one)));
+            if (p.dz_part)
+                *reinterpret_cast<float2*>(p.dz_part + un.kb * LD + at) = dz;
             else
-                *reinterpret_cast<raw*>(static_cast<io_t*>(p.g.du) + un.ub * p.L * p.D + at) =
-                    P2::r(make_float2(du[0], du[1]));
-            *reinterpret_cast<raw*>(static_cast<io_t*>(p.g.ddelta) + (un.kb * p.L + t + r) * p.D +
-                                    un.c0 + c) = P2::r(make_float2(dl[0], dl[1]));
-            if (p.z) {
-                if (p.dz_part)
-                    *reinterpret_cast<float2*>(p.dz_part + un.kb * p.L * p.D + at) =
-                        make_float2(dz[0], dz[1]);
-                else
-                    *reinterpret_cast<raw*>(static_cast<io_t*>(p.g.dz) + un.b * p.L * p.D + at) =
-                        P2::r(make_float2(dz[0], dz[1]));
-            }
+                *reinterpret_cast<raw*>(static_cast<io_t*>(p.g.dz) + un.b * LD + at) = P2::r(dz);
         }
-    // dB and dC: a pair of threads adds the 32 partial rows of one (step, tensor, 4 states)
-    const int half = (lane >> 2) & 1, n4 = 4 * (lane & 3);
-    const int which = warp * 4 + (lane >> 3);
-    const int r = which >> 1, q = which & 1;
+    }
+    // a lane adds the 8 channel pairs of one (step, tensor, 4 states); the lanes of the two
+    // tensors start one row apart, so that their banks differ
+    const int n4 = x.lane & 3, q = (x.lane >> 2) & 1, step = x.lane >> 3;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < kBwdThreads / 8; ++i) {
-        const float4 w = *reinterpret_cast<const float4*>(&sm.dbc[r][q][2 * i + half][n4]);
+    for (int i = 0; i < kWC / 2; ++i) {
+        const float4 w = *reinterpret_cast<const float4*>(
+            &sm.dbc[x.warp][step][q][(i + q) & (kWC / 2 - 1)][4 * n4]);
         v.x += w.x;
         v.y += w.y;
         v.z += w.z;
         v.w += w.w;
     }
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, 4);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, 4);
-    v.z += __shfl_xor_sync(0xffffffffu, v.z, 4);
-    v.w += __shfl_xor_sync(0xffffffffu, v.w, 4);
-    if (half == 0 && r < rows)
-        *reinterpret_cast<float4*>(p.dbc + ((un.kb * un.ctiles + un.ctile) * p.L + t + r) * 2 * kNP +
-                                   q * kNP + n4) = v;
+    sm.acc[r0 + step][q][x.warp][n4] = v;
+}
+
+// dB and dC of a finished tile: the sums of the four warps, to the CTA's partial sums.
+template <typename io_t>
+__device__ __forceinline__ void store_dbc(const BwdParams& p, const Unit& un, int t, GradSmem<io_t>& sm)
+{
+    const int rows = min(un.t1 - t, kTL);
+    float* out = p.dbc + ((un.kb * un.ctiles + un.ctile) * p.L + t) * (2 * kNP);
+    constexpr int kVec = 2 * kNP / 4;  // float4 of a step
+    for (int j = threadIdx.x; j < rows * kVec; j += kBwdThreads) {
+        const int r = j / kVec, q = (j / (kNP / 4)) & 1, n4 = j & (kNP / 4 - 1);
+        float4 v = sm.acc[r][q][0][n4];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+            const float4 a = sm.acc[r][q][w][n4];
+            v.x += a.x;
+            v.y += a.y;
+            v.z += a.z;
+            v.w += a.w;
+        }
+        *reinterpret_cast<float4*>(out + 4 * j) = v;
+    }
 }
 
 template <typename io_t, bool SPLIT>
-__global__ void __launch_bounds__(kBwdThreads) grad_kernel(const __grid_constant__ BwdParams p)
+__global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_constant__ BwdParams p)
 {
+    constexpr bool PRECISE = std::is_same<io_t, float>::value;
     extern __shared__ __align__(128) unsigned char raw_smem[];
     GradSmem<io_t>& sm = *reinterpret_cast<GradSmem<io_t>*>(raw_smem);
     const Unit un = unit_of(p);
-    const Cell x = cell_of();
-    const Par par = load_par(p, un);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float2 A2[2][2], g[2][2], dA[2][2], hstart[2][2];
-    load_A2(p, un, x, A2);
+    const Cell x = cell_of(un);
+    const Par par = load_par(p, un, x);
+    float2 A[4], g[4], dA[4], hstart[4];
+    load_A<PRECISE>(p, un, x, A);
     float2 dskip = dup(0.f), dbias = dup(0.f);
 
     // the state that enters the segment and the gradient that enters it from behind
     const bool shift = SPLIT && (un.seg > 0 || p.init != nullptr);
+    const int64_t cell = (un.kb * p.D + un.c0 + x.c) * p.N;  // of [K, batch, D, N] arrays
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        float hv[4], gv[4];
-        const int64_t at = (un.kb * p.D + un.c0 + x.c[j]) * p.N + 4 * x.ng;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool ok = x.c[j] < un.cv && 4 * x.ng + i < p.N;
-            hv[i] = ok && p.init ? p.init[at + i] : 0.f;
-            gv[i] = ok && p.dlast ? p.dlast[at + i] : 0.f;
+    for (int i = 0; i < 4; ++i) {
+        const int n = 4 * x.ng + i;
+        hstart[i] = g[i] = dA[i] = dup(0.f);
+        if (x.valid && n < p.N) {
+            if (p.init)
+                hstart[i] = make_float2(p.init[cell + n], p.init[cell + p.N + n]);
+            if (p.dlast)
+                g[i] = make_float2(p.dlast[cell + n], p.dlast[cell + p.N + n]);
         }
+    }
+    if (SPLIT) {
+        float2 P[4], v[4];
+        for (int s = 0; s < un.seg; ++s) {
+            get4(seg_at(p.seg_p, p, un, s), kBwdThreads, P);
+            get4(seg_at(p.seg_h, p, un, s), kBwdThreads, v);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            hstart[j][i] = make_float2(hv[2 * i], hv[2 * i + 1]);
-            g[j][i] = make_float2(gv[2 * i], gv[2 * i + 1]);
-            dA[j][i] = dup(0.f);
+            for (int i = 0; i < 4; ++i)
+                hstart[i] = __ffma2_rn(P[i], hstart[i], v[i]);
         }
-        if (SPLIT && x.c[j] < un.cv) {
-            for (int s = 0; s < un.seg; ++s) {
-                const int64_t o = seg_at(p, un, x, s, j);
-                const float4 P = *reinterpret_cast<const float4*>(p.seg_p + o);
-                const float4 H = *reinterpret_cast<const float4*>(p.seg_h + o);
-                hstart[j][0] = __ffma2_rn(make_float2(P.x, P.y), hstart[j][0], make_float2(H.x, H.y));
-                hstart[j][1] = __ffma2_rn(make_float2(P.z, P.w), hstart[j][1], make_float2(H.z, H.w));
-            }
-            for (int s = p.S - 1; s > un.seg; --s) {
-                const int64_t o = seg_at(p, un, x, s, j);
-                const float4 P = *reinterpret_cast<const float4*>(p.seg_p + o);
-                const float4 G = *reinterpret_cast<const float4*>(p.seg_g + o);
-                g[j][0] = __ffma2_rn(make_float2(P.x, P.y), g[j][0], make_float2(G.x, G.y));
-                g[j][1] = __ffma2_rn(make_float2(P.z, P.w), g[j][1], make_float2(G.z, G.w));
-            }
+        for (int s = p.S - 1; s > un.seg; --s) {
+            get4(seg_at(p.seg_p, p, un, s), kBwdThreads, P);
+            get4(seg_at(p.seg_g, p, un, s), kBwdThreads, v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                g[i] = __ffma2_rn(P[i], g[i], v[i]);
         }
     }
 
-    const int64_t ntile = (un.t1 - un.t0 + kT - 1) / kT;
-    io_t bc[2];
-    issue<io_t, true>(p, un, un.tile0 + ntile - 1, sm.st[(ntile - 1) & 1], true, bc);
-    for (int64_t it = ntile - 1; it >= 0; --it) {
-        const int64_t tile = un.tile0 + it;
+    const int tiles = (un.t1 - un.t0 + kTL - 1) / kTL;
+    int slice = (un.t1 - 1) / kT;  // of the sequence; segments start on slice borders
+    // the next slice's checkpoint is on its way while this one is worked on
+    float2 next[4], next_cum = dup(0.f);
+    get4(ckpt_at(p, un, slice), kBwdThreads, next);
+    if (shift && x.valid)
+        next_cum = *cum_at(p, un, x, slice);
+    io_t bc[kBC][2];
+    issue<io_t>(p, un, un.t0 + (tiles - 1) * kTL, sm.st[(tiles - 1) & 1], true, bc);
+    for (int it = tiles - 1; it >= 0; --it) {
+        const int t = un.t0 + it * kTL;
         const Stage<io_t>& st = sm.st[it & 1];
         cp_wait_all();
         __syncthreads();
-        // the sums of the tile done before this one, while its rows are still in their stage
-        if (it + 1 < ntile) {
-            finish_tile(p, un, tile + 1, sm, sm.st[(it + 1) & 1], par, dskip, dbias);
-            __syncthreads();  // scal is rewritten below
-        }
-        prepass(p, un, tile, sm, st, par, true, bc);
+        if (it + 1 < tiles)
+            store_dbc(p, un, t + kTL, sm);
+        prepass(p, un, x, t, sm, st, par, true, bc);
         __syncthreads();
         if (it > 0)
-            issue<io_t, true>(p, un, tile - 1, sm.st[(it - 1) & 1], true, bc);
+            issue<io_t>(p, un, t - kTL, sm.st[(it - 1) & 1], true, bc);
 
-        // the tile's states, from its checkpoint
-        float2 h[kT + 1][2][2], a[kT][2][2];
+        for (int r0 = kTL - kT; r0 >= 0; r0 -= kT) {
+            if (t + r0 >= un.t1)
+                continue;
+            // the slice's states, from its checkpoint
+            float2 h[kT + 1][4], a[kT][4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float4 ck = st.ckpt[j][threadIdx.x];
-            h[0][j][0] = make_float2(ck.x, ck.y);
-            h[0][j][1] = make_float2(ck.z, ck.w);
+            for (int i = 0; i < 4; ++i)
+                h[0][i] = next[i];
             if (shift) {
-                const float cum = x.c[j] < un.cv
-                                      ? p.cum[(un.kb * un.ntiles + tile) * p.D + un.c0 + x.c[j]]
-                                      : 0.f;
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    h[0][j][i] = __ffma2_rn(ex2_2(__fmul2_rn(dup(cum), A2[j][i])), hstart[j][i],
-                                            h[0][j][i]);
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < kT; ++r) {
-            const float4 B4 = *reinterpret_cast<const float4*>(&sm.B[r][4 * x.ng]);
-            const float2 B[2] = {make_float2(B4.x, B4.y), make_float2(B4.z, B4.w)};
-            const float4 C4 = *reinterpret_cast<const float4*>(&sm.C[r][4 * x.ng]);
-            const float2 C[2] = {make_float2(C4.x, C4.y), make_float2(C4.z, C4.w)};
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float4 s = sm.scal[r][x.c[j]];
-                float2 y = dup(0.f);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    a[r][j][i] = ex2_2(__fmul2_rn(dup(s.x), A2[j][i]));
-                    h[r + 1][j][i] = __ffma2_rn(a[r][j][i], h[r][j][i], __fmul2_rn(dup(s.y), B[i]));
-                    y = __ffma2_rn(C[i], h[r + 1][j][i], y);
+                for (int i = 0; i < 4; ++i) {
+                    const float2 d = decay<PRECISE>(next_cum, A[i]);
+                    h[0][i] = __fadd2_rn(h[0][i], decayed<PRECISE>(d, hstart[i]));
                 }
-                if (p.z)
-                    sm.part[0][r][x.c[j]][x.ng] = y.x + y.y;
             }
-        }
-        // the reverse recurrence
+            if (t + r0 > un.t0) {
+                --slice;
+                get4(ckpt_at(p, un, slice), kBwdThreads, next);
+                if (shift && x.valid)
+                    next_cum = *cum_at(p, un, x, slice);
+            }
 #pragma unroll
-        for (int r = kT - 1; r >= 0; --r) {
-            const float4 B4 = *reinterpret_cast<const float4*>(&sm.B[r][4 * x.ng]);
-            const float2 B[2] = {make_float2(B4.x, B4.y), make_float2(B4.z, B4.w)};
-            const float4 C4 = *reinterpret_cast<const float4*>(&sm.C[r][4 * x.ng]);
-            const float2 C[2] = {make_float2(C4.x, C4.y), make_float2(C4.z, C4.w)};
-            float2 dB[2] = {dup(0.f), dup(0.f)}, dC[2] = {dup(0.f), dup(0.f)};
+            for (int r = 0; r < kT; ++r) {
+                float2 B[4], C[4], y;
+                load4(sm.B, r0 + r, x.ng, B);
+                const float2 dl = sm.scal[x.warp][r0 + r][0][x.cg];
+                const float2 w = sm.scal[x.warp][r0 + r][1][x.cg];
+                load4(sm.C, r0 + r, x.ng, C);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float4 s = sm.scal[r][x.c[j]];
-                float2 gB = dup(0.f), gA = dup(0.f);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    g[j][i] = __ffma2_rn(dup(s.z), C[i], g[j][i]);
-                    dC[i] = __ffma2_rn(dup(s.z), h[r + 1][j][i], dC[i]);
-                    dB[i] = __ffma2_rn(dup(s.y), g[j][i], dB[i]);
-                    gB = __ffma2_rn(g[j][i], B[i], gB);
-                    g[j][i] = __fmul2_rn(g[j][i], a[r][j][i]);
-                    const float2 q = __fmul2_rn(g[j][i], h[r][j][i]);
-                    gA = __ffma2_rn(q, A2[j][i], gA);
-                    dA[j][i] = __ffma2_rn(q, dup(s.x), dA[j][i]);
+                for (int i = 0; i < 4; ++i) {
+                    a[r][i] = decay<PRECISE>(dl, A[i]);
+                    h[r + 1][i] = decayed<PRECISE>(a[r][i], h[r][i], __fmul2_rn(w, B[i]));
+                    y = i ? __ffma2_rn(C[i], h[r + 1][i], y) : __fmul2_rn(C[i], h[r + 1][i]);
                 }
-                sm.part[1][r][x.c[j]][x.ng] = gB.x + gB.y;
-                sm.part[2][r][x.c[j]][x.ng] = gA.x + gA.y;
+                *reinterpret_cast<float2*>(&sm.part[x.warp][0][r][x.ng * kWC + 2 * x.cg]) = y;
             }
-            const int row = warp * 8 + (lane >> 2);
-            *reinterpret_cast<float4*>(&sm.dbc[r][0][row][4 * x.ng]) =
-                make_float4(dB[0].x, dB[0].y, dB[1].x, dB[1].y);
-            *reinterpret_cast<float4*>(&sm.dbc[r][1][row][4 * x.ng]) =
-                make_float4(dC[0].x, dC[0].y, dC[1].x, dC[1].y);
+            // the reverse recurrence
+#pragma unroll
+            for (int r = kT - 1; r >= 0; --r) {
+                float2 B[4], C[4], gB, gA;
+                load4(sm.B, r0 + r, x.ng, B);
+                load4(sm.C, r0 + r, x.ng, C);
+                const float2 dl = sm.scal[x.warp][r0 + r][0][x.cg];
+                const float2 w = sm.scal[x.warp][r0 + r][1][x.cg];
+                const float2 dy = sm.scal[x.warp][r0 + r][2][x.cg];
+                float dB[4], dC[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    g[i] = __ffma2_rn(dy, C[i], g[i]);
+                    const float2 c2 = __fmul2_rn(dy, h[r + 1][i]), b2 = __fmul2_rn(w, g[i]);
+                    dC[i] = c2.x + c2.y;
+                    dB[i] = b2.x + b2.y;
+                    gB = i ? __ffma2_rn(g[i], B[i], gB) : __fmul2_rn(g[i], B[i]);
+                    g[i] = decayed<PRECISE>(a[r][i], g[i]);
+                    const float2 q = __fmul2_rn(g[i], h[r][i]);
+                    gA = i ? __ffma2_rn(q, A[i], gA) : __fmul2_rn(q, A[i]);
+                    dA[i] = __ffma2_rn(q, dl, dA[i]);
+                }
+                *reinterpret_cast<float2*>(&sm.part[x.warp][1][r][x.ng * kWC + 2 * x.cg]) = gB;
+                *reinterpret_cast<float2*>(&sm.part[x.warp][2][r][x.ng * kWC + 2 * x.cg]) = gA;
+                *reinterpret_cast<float4*>(&sm.dbc[x.warp][r][0][x.cg][4 * x.ng]) =
+                    make_float4(dB[0], dB[1], dB[2], dB[3]);
+                *reinterpret_cast<float4*>(&sm.dbc[x.warp][r][1][x.cg][4 * x.ng]) =
+                    make_float4(dC[0], dC[1], dC[2], dC[3]);
+            }
+            __syncwarp();
+            finish_slice(p, un, x, t + r0, r0, sm, st, par, dskip, dbias);
+            __syncwarp();
         }
     }
     __syncthreads();
-    finish_tile(p, un, un.tile0, sm, sm.st[0], par, dskip, dbias);
+    store_dbc(p, un, un.t0, sm);
 
     // what the segment leaves: the initial state's gradient and its parameter gradients
-    const int64_t row = un.kb * p.S + un.seg;
+    float* par_out = p.dpar + ((un.kb * p.S + un.seg) * p.D + un.c0 + x.c) * (kNP + 2);
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = 4 * x.ng + i;
-            if (x.c[j] < un.cv && n < p.N) {
-                const float2 gv = g[j][i / 2], av = dA[j][i / 2];
-                const int64_t d = un.c0 + x.c[j];
-                if (p.g.dinitial_state && un.seg == 0)
-                    p.g.dinitial_state[(un.kb * p.D + d) * p.N + n] = i & 1 ? gv.y : gv.x;
-                p.dpar[(row * p.D + d) * (kNP + 2) + n] = i & 1 ? av.y : av.x;
+    for (int i = 0; i < 4; ++i) {
+        const int n = 4 * x.ng + i;
+        if (x.valid && n < p.N) {
+            if (p.g.dinitial_state && un.seg == 0) {
+                p.g.dinitial_state[cell + n] = g[i].x;
+                p.g.dinitial_state[cell + p.N + n] = g[i].y;
             }
+            par_out[n] = dA[i].x;
+            par_out[kNP + 2 + n] = dA[i].y;
         }
-    __syncthreads();  // part is free again
-    float* red = &sm.part[0][0][0][0];
-    const int c = 2 * lane;
-    red[warp * kC + c] = dskip.x;
-    red[warp * kC + c + 1] = dskip.y;
-    red[(4 + warp) * kC + c] = dbias.x;
-    red[(4 + warp) * kC + c + 1] = dbias.y;
-    __syncthreads();
-    const int cc = threadIdx.x & (kC - 1), q = threadIdx.x / kC;
-    if (cc < un.cv) {
-        const float* r4 = red + 4 * q * kC + cc;
-        p.dpar[(row * p.D + un.c0 + cc) * (kNP + 2) + kNP + q] =
-            (r4[0] + r4[kC]) + (r4[2 * kC] + r4[3 * kC]);
+    }
+#pragma unroll
+    for (int m = 1; m < 4; m *= 2) {
+        dskip.x += __shfl_xor_sync(0xffffffffu, dskip.x, m);
+        dskip.y += __shfl_xor_sync(0xffffffffu, dskip.y, m);
+        dbias.x += __shfl_xor_sync(0xffffffffu, dbias.x, m);
+        dbias.y += __shfl_xor_sync(0xffffffffu, dbias.y, m);
+    }
+    if (x.ng == 0 && x.valid) {
+        par_out[kNP] = dskip.x;
+        par_out[kNP + 1] = dbias.x;
+        par_out[kNP + 2 + kNP] = dskip.y;
+        par_out[kNP + 2 + kNP + 1] = dbias.y;
     }
 }
 
