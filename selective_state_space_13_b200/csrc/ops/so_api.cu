@@ -121,11 +121,30 @@ struct BwdPlan {
     size_t off_ckpt, off_cum, off_h, off_p, off_g, off_dbc, off_dpar, off_du, off_dz, bytes;
 };
 
-// Sequences are split while the (direction, batch row, channel tile) units fill less than half of
-// the three CTAs that fit on each of the 148 SMs: into as many segments as fill them once, of at
-// least 64 steps.
+// Automatic segments of the gradient. `units` (direction, batch row, channel tile) CTAs for each
+// segment fill the kBwdSlots CTAs that fit on a B200 (3 on each of 148 SMs) in whole waves: S
+// segments take ceil(units S / slots) / S of a whole sequence's time, any split costs about 15%
+// more work (the segment products, the checkpoints' shift) and each segment 1% (its ends).  Measured, 8 x 2048 x 1536 (192 units):
+// 1434 us unsplit, 923 at S = 2, 887 at 4, 820 at 6, 800 at 9; 64 x 197 x 768 in two directions (1536
+// units): 623 us unsplit, more with any split.  No segment is shorter than 64 steps.
 constexpr int64_t kBwdSlots = 3 * 148;
 constexpr int64_t kBwdMinSteps = 64;
+constexpr int64_t kBwdMostAuto = 32;
+
+int64_t bwd_segments(int64_t units, int64_t L)
+{
+    int64_t best = 1;
+    double least = static_cast<double>(ceil_div(units, kBwdSlots));
+    for (int64_t S = 2; S <= kBwdMostAuto && S <= L / kBwdMinSteps; ++S) {
+        const double cost =
+            (1.15 + 0.01 * S) * static_cast<double>(ceil_div(units * S, kBwdSlots)) / S;
+        if (cost < 0.999 * least) {
+            least = cost;
+            best = S;
+        }
+    }
+    return best;
+}
 
 ss_status plan_bwd(const ss_shape* s, const ss_direction_map* dmap, const ss_launch_opts* o,
                    bool gate, BwdPlan* pl)
@@ -166,11 +185,8 @@ ss_status plan_bwd(const ss_shape* s, const ss_direction_map* dmap, const ss_lau
     const int64_t L = s->seqlen, rows = s->batch * pl->K;
     const int64_t ctiles = ceil_div(s->dim, so::kBwdChannels), ntiles = ceil_div(L, so::kBwdTile);
     const int64_t units = rows * ctiles;
-    if (want == 0) {
-        want = units > 0 && units < kBwdSlots / 2 ? kBwdSlots / units : 1;
-        if (want > L / kBwdMinSteps)
-            want = L / kBwdMinSteps;
-    }
+    if (want == 0)
+        want = bwd_segments(units, L);
     if (want > kMaxSegments)
         want = kMaxSegments;
     if (want > ntiles)

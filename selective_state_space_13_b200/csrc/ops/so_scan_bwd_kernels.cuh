@@ -124,20 +124,76 @@ template <typename io_t> struct Stage {
     io_t u[kTL][kPitch], delta[kTL][kPitch], dout[kTL][kPitch], z[kTL][kPitch];
 };
 
+// What a CTA needs now and then: kept in shared memory and read there each time (volatile), so that
+// it takes no registers from the recurrences.
+struct Cta {
+    const void *u, *delta, *dout, *z;  // first element of the CTA's rows and channels
+    void *du, *ddelta, *dz;            // (du, dz: io rows or fp32 parts)
+    const void *B, *C;
+    float* dbc;
+    float4* ckpt;
+    float* cum;
+    float skip[kC], bias[kC];
+};
+
+template <typename T> __device__ __forceinline__ T again(const T& v)
+{
+    return *const_cast<const volatile T*>(&v);
+}
+
+__device__ __forceinline__ float2 again2(const float* v)
+{
+    return make_float2(again(v[0]), again(v[1]));
+}
+
 template <typename io_t> struct SumSmem {
+    Cta cta;
     Stage<io_t> st[2];
-    float2 B[kTL][kNP], C[kTL][kNP];       // duplicated
+    float B[kTL][kNP], C[kTL][kNP];
     float2 scal[kWarps][kTL][3][kWC / 2];  // Delta, Delta u, dy of a channel pair
 };
 
 template <typename io_t> struct GradSmem {
+    Cta cta;
     Stage<io_t> st[2];
-    float2 B[kTL][kNP], C[kTL][kNP];
+    float B[kTL][kNP], C[kTL][kNP];
     float2 scal[kWarps][kTL][3][kWC / 2];
     float part[kWarps][3][kT][kPartPitch];  // y, sum g B, sum g A Abar h: [state group][channel]
     float dbc[kWarps][kT][2][kWC / 2][kNP]; // dB, dC of every channel pair
     float4 acc[kTL][2][kWarps][kNP / 4];    // dB, dC of every warp
+    float4 hstart[2][kBwdThreads];          // the state that enters the segment (SPLIT)
 };
+
+// The CTA's bases and parameters, written once.
+template <typename io_t>
+__device__ __forceinline__ void fill_cta(const BwdParams& p, const Unit& un, Cta& c)
+{
+    const int64_t LD = p.L * p.D, nslices = (p.L + kT - 1) / kT;
+    if (threadIdx.x == 0) {
+        c.u = static_cast<const io_t*>(p.u) + un.ub * LD + un.c0;
+        c.delta = static_cast<const io_t*>(p.delta) + un.kb * LD + un.c0;
+        c.dout = static_cast<const io_t*>(p.dout) + un.b * LD + un.c0;
+        c.z = static_cast<const io_t*>(p.z) + (p.z ? un.b * LD + un.c0 : 0);
+        c.du = p.du_part ? static_cast<void*>(p.du_part + un.kb * LD + un.c0)
+                         : static_cast<io_t*>(p.g.du) + un.ub * LD + un.c0;
+        c.ddelta = static_cast<io_t*>(p.g.ddelta) + un.kb * LD + un.c0;
+        c.dz = p.dz_part ? static_cast<void*>(p.dz_part + un.kb * LD + un.c0)
+                         : static_cast<io_t*>(p.g.dz) + (p.z ? un.b * LD + un.c0 : 0);
+        c.B = static_cast<const io_t*>(p.B) + un.kb * p.L * p.N;
+        c.C = static_cast<const io_t*>(p.C) + un.kb * p.L * p.N;
+        c.dbc = p.dbc + (un.kb * un.ctiles + un.ctile) * p.L * (2 * kNP);
+        c.ckpt = reinterpret_cast<float4*>(p.ckpt) +
+                 (un.kb * nslices * un.ctiles + un.ctile) * (2 * kBwdThreads);
+        c.cum = p.cum + un.kb * nslices * p.D + un.c0;
+    }
+    if (threadIdx.x < kC) {
+        const int64_t d = (p.params_per_dir ? un.k * p.D : 0) + un.c0 + threadIdx.x;
+        const bool ok = threadIdx.x < un.cv;
+        c.skip[threadIdx.x] = ok && p.Dskip ? p.Dskip[d] : 0.f;
+        c.bias[threadIdx.x] = ok && p.bias ? p.bias[d] : 0.f;
+    }
+    __syncthreads();
+}
 
 // Starts the copies of the tile of steps t..t+kTL-1 into a stage; returns the raw B and C elements
 // that this thread will convert.
@@ -145,17 +201,16 @@ constexpr int kBC = kTL * kNP / kBwdThreads;
 static_assert(kBC * kBwdThreads == kTL * kNP, "whole rounds of B and C elements");
 
 template <typename io_t>
-__device__ __forceinline__ void issue(const BwdParams& p, const Unit& un, int t, Stage<io_t>& st,
-                                      bool want_dy, io_t (*bc)[2])
+__device__ __forceinline__ void issue(const BwdParams& p, const Unit& un, const Cta& cta, int t,
+                                      Stage<io_t>& st, bool want_dy, io_t (*bc)[2])
 {
     constexpr int E = 16 / sizeof(io_t);  // elements of a 16-byte piece
     constexpr int PR = kC / E;            // pieces of a row
     const int rows = min(un.t1 - t, kTL);
-    const int64_t LD = p.L * p.D;
-    const io_t* gu = static_cast<const io_t*>(p.u) + un.ub * LD + un.c0;
-    const io_t* gl = static_cast<const io_t*>(p.delta) + un.kb * LD + un.c0;
-    const io_t* go = static_cast<const io_t*>(p.dout) + un.b * LD + un.c0;
-    const io_t* gz = p.z ? static_cast<const io_t*>(p.z) + un.b * LD + un.c0 : nullptr;
+    const io_t* gu = static_cast<const io_t*>(again(cta.u));
+    const io_t* gl = static_cast<const io_t*>(again(cta.delta));
+    const io_t* go = static_cast<const io_t*>(again(cta.dout));
+    const io_t* gz = static_cast<const io_t*>(again(cta.z));
 #pragma unroll
     for (int i = 0; i < (kTL * PR + kBwdThreads - 1) / kBwdThreads; ++i) {
         const int j = threadIdx.x + i * kBwdThreads;
@@ -167,20 +222,21 @@ __device__ __forceinline__ void issue(const BwdParams& p, const Unit& un, int t,
             cp16(&st.delta[r][c], gl + (ok ? static_cast<uint32_t>(t + r) * un.D + c : 0u), ok);
             if (want_dy) {
                 cp16(&st.dout[r][c], go + at, ok);
-                if (gz)
+                if (p.z)
                     cp16(&st.z[r][c], gz + at, ok);
             }
         }
     }
     cp_commit();
-    const io_t* gB = static_cast<const io_t*>(p.B) + (un.kb * p.L + t) * p.N;
-    const io_t* gC = static_cast<const io_t*>(p.C) + (un.kb * p.L + t) * p.N;
+    const io_t* gB = static_cast<const io_t*>(again(cta.B));
+    const io_t* gC = static_cast<const io_t*>(again(cta.C));
 #pragma unroll
     for (int i = 0; i < kBC; ++i) {
         const int j = threadIdx.x + i * kBwdThreads, r = j / kNP, n = j % kNP;
         const bool ok = r < rows && n < p.N;
-        bc[i][0] = ok ? gB[r * p.N + n] : io_t(0.f);
-        bc[i][1] = ok ? gC[r * p.N + n] : io_t(0.f);
+        const int64_t at = static_cast<int64_t>(t + r) * p.N + n;
+        bc[i][0] = ok ? gB[at] : io_t(0.f);
+        bc[i][1] = ok ? gC[at] : io_t(0.f);
     }
 }
 
@@ -201,25 +257,6 @@ __device__ __forceinline__ Cell cell_of(const Unit& un)
     x.c = x.warp * kWC + 2 * x.cg;
     x.valid = x.c < un.cv;
     return x;
-}
-
-// Per-channel parameters of the thread's channel pair.
-struct Par {
-    float2 skip, bias;
-};
-
-__device__ __forceinline__ Par load_par(const BwdParams& p, const Unit& un, const Cell& x)
-{
-    const int64_t d = (p.params_per_dir ? un.k * p.D : 0) + un.c0 + x.c;
-    Par q;
-    q.skip = q.bias = dup(0.f);
-    if (x.valid) {
-        if (p.Dskip)
-            q.skip = make_float2(p.Dskip[d], p.Dskip[d + 1]);
-        if (p.bias)
-            q.bias = make_float2(p.bias[d], p.bias[d + 1]);
-    }
-    return q;
 }
 
 // A of the thread's cells, times log2(e) for the exponentials in base 2 (not for fp32 io, which
@@ -287,15 +324,16 @@ __device__ __forceinline__ float2 softplus_2(float2 x)
 // the segment and channels behind the row become Delta = 0, a step that changes nothing.
 template <typename io_t, typename Smem>
 __device__ __forceinline__ void prepass(const BwdParams& p, const Unit& un, const Cell& x, int t,
-                                        Smem& sm, const Stage<io_t>& st, const Par& par,
-                                        bool want_dy, const io_t (*bc)[2])
+                                        Smem& sm, const Stage<io_t>& st, bool want_dy,
+                                        const io_t (*bc)[2])
 {
     const int rows = min(un.t1 - t, kTL);
+    const float2 bias = again2(&sm.cta.bias[x.c]);
 #pragma unroll
     for (int r = x.ng; r < kTL; r += kT) {
         float2 dl = dup(0.f), w = dl, dy = dl;
         if (r < rows && x.valid) {
-            dl = __fadd2_rn(pair_at(&st.delta[r][x.c]), par.bias);
+            dl = __fadd2_rn(pair_at(&st.delta[r][x.c]), bias);
             if (p.softplus)
                 dl = softplus_2(dl);
             w = __fmul2_rn(dl, pair_at(&st.u[r][x.c]));
@@ -315,20 +353,19 @@ __device__ __forceinline__ void prepass(const BwdParams& p, const Unit& un, cons
 #pragma unroll
     for (int i = 0; i < kBC; ++i) {
         const int j = threadIdx.x + i * kBwdThreads;
-        sm.B[j / kNP][j % kNP] = dup(ld1(&bc[i][0]));
-        sm.C[j / kNP][j % kNP] = dup(ld1(&bc[i][1]));
+        sm.B[j / kNP][j % kNP] = ld1(&bc[i][0]);
+        sm.C[j / kNP][j % kNP] = ld1(&bc[i][1]);
     }
 }
 
-// The thread's 4 duplicated elements of a row of B or C.
-__device__ __forceinline__ void load4(const float2 (*rows)[kNP], int r, int ng, float2 v[4])
+// The thread's 4 elements of a row of B or C, each for both channels.
+__device__ __forceinline__ void load4(const float (*rows)[kNP], int r, int ng, float2 v[4])
 {
     const float4 a = *reinterpret_cast<const float4*>(&rows[r][4 * ng]);
-    const float4 b = *reinterpret_cast<const float4*>(&rows[r][4 * ng + 2]);
-    v[0] = make_float2(a.x, a.y);
-    v[1] = make_float2(a.z, a.w);
-    v[2] = make_float2(b.x, b.y);
-    v[3] = make_float2(b.z, b.w);
+    v[0] = dup(a.x);
+    v[1] = dup(a.y);
+    v[2] = dup(a.z);
+    v[3] = dup(a.w);
 }
 
 // Per-thread arrays in global memory as two float4 per cell block.
@@ -347,24 +384,22 @@ __device__ __forceinline__ void get4(const float4* at, int stride, float2 v[4])
     v[3] = make_float2(b.z, b.w);
 }
 
-// Checkpoint of this thread for slice `s` of the sequence, and the block of a segment.
-__device__ __forceinline__ float4* ckpt_at(const BwdParams& p, const Unit& un, int s)
+// Checkpoint of this thread for slice `s` of the sequence, the sums of Delta there, and the block
+// of a segment.
+__device__ __forceinline__ float4* ckpt_at(const Unit& un, const Cta& cta, int s)
 {
-    const int64_t nslices = (p.L + kT - 1) / kT;
-    return reinterpret_cast<float4*>(p.ckpt) +
-           ((un.kb * nslices + s) * un.ctiles + un.ctile) * (2 * kBwdThreads) + threadIdx.x;
+    return again(cta.ckpt) + static_cast<int64_t>(s) * un.ctiles * (2 * kBwdThreads) + threadIdx.x;
+}
+
+__device__ __forceinline__ float2* cum_at(const Unit& un, const Cta& cta, const Cell& x, int s)
+{
+    return reinterpret_cast<float2*>(again(cta.cum) + static_cast<int64_t>(s) * un.D + x.c);
 }
 
 __device__ __forceinline__ float4* seg_at(float* base, const BwdParams& p, const Unit& un, int seg)
 {
     return reinterpret_cast<float4*>(base) +
            ((un.kb * p.S + seg) * un.ctiles + un.ctile) * (2 * kBwdThreads) + threadIdx.x;
-}
-
-__device__ __forceinline__ float2* cum_at(const BwdParams& p, const Unit& un, const Cell& x, int s)
-{
-    const int64_t nslices = (p.L + kT - 1) / kT;
-    return reinterpret_cast<float2*>(p.cum + (un.kb * nslices + s) * p.D + un.c0 + x.c);
 }
 
 // ------------------------------------------------------------------------- summary sweep
@@ -377,7 +412,7 @@ __global__ void __launch_bounds__(kBwdThreads) summary_kernel(const __grid_const
     SumSmem<io_t>& sm = *reinterpret_cast<SumSmem<io_t>*>(raw_smem);
     const Unit un = unit_of(p);
     const Cell x = cell_of(un);
-    const Par par = load_par(p, un, x);
+    fill_cta<io_t>(p, un, sm.cta);
     float2 A[4], h[4], P[4], G[4], cum = dup(0.f);
     load_A<PRECISE>(p, un, x, A);
 #pragma unroll
@@ -386,20 +421,20 @@ __global__ void __launch_bounds__(kBwdThreads) summary_kernel(const __grid_const
         P[i] = dup(1.f);
     }
     io_t bc[kBC][2];
-    issue<io_t>(p, un, un.t0, sm.st[0], SPLIT, bc);
+    issue<io_t>(p, un, sm.cta, un.t0, sm.st[0], SPLIT, bc);
     for (int t = un.t0, it = 0; t < un.t1; t += kTL, ++it) {
         cp_wait_all();
         __syncthreads();
-        prepass(p, un, x, t, sm, sm.st[it & 1], par, SPLIT, bc);
+        prepass(p, un, x, t, sm, sm.st[it & 1], SPLIT, bc);
         __syncthreads();
         if (t + kTL < un.t1)
-            issue<io_t>(p, un, t + kTL, sm.st[(it + 1) & 1], SPLIT, bc);
+            issue<io_t>(p, un, sm.cta, t + kTL, sm.st[(it + 1) & 1], SPLIT, bc);
 #pragma unroll
         for (int r = 0; r < kTL; ++r) {
             if (r % kT == 0 && t + r < un.t1) {
-                put4(ckpt_at(p, un, (t + r) / kT), kBwdThreads, h);
+                put4(ckpt_at(un, sm.cta, (t + r) / kT), kBwdThreads, h);
                 if (SPLIT && x.ng == 0 && x.valid)
-                    *cum_at(p, un, x, (t + r) / kT) = cum;
+                    *cum_at(un, sm.cta, x, (t + r) / kT) = cum;
             }
             float2 B[4], C[4];
             load4(sm.B, r, x.ng, B);
@@ -435,7 +470,7 @@ __global__ void __launch_bounds__(kBwdThreads) summary_kernel(const __grid_const
 template <typename io_t>
 __device__ __forceinline__ void finish_slice(const BwdParams& p, const Unit& un, const Cell& x, int t,
                                              int r0, GradSmem<io_t>& sm, const Stage<io_t>& st,
-                                             const Par& par, float2& dskip, float2& dbias)
+                                             float2& dskip, float2& dbias)
 {
     using P2 = Pair<io_t>;
     using raw = typename P2::raw;
@@ -456,31 +491,34 @@ __device__ __forceinline__ void finish_slice(const BwdParams& p, const Unit& un,
         float2 gA = sum(2);
         if (!PRECISE)
             gA = __fmul2_rn(gA, dup(kLn2));  // A was in base 2
-        const float2 du = __ffma2_rn(par.skip, dy, __fmul2_rn(dl, gB));
+        const float2 skip = again2(&sm.cta.skip[x.c]);
+        const float2 du = __ffma2_rn(skip, dy, __fmul2_rn(dl, gB));
         float2 dd = __ffma2_rn(u, gB, gA);
         if (p.softplus)
-            dd = __fmul2_rn(dd, sigmoid_2(__fadd2_rn(pair_at(&st.delta[r][x.c]), par.bias)));
+            dd = __fmul2_rn(dd, sigmoid_2(__fadd2_rn(pair_at(&st.delta[r][x.c]),
+                                                  again2(&sm.cta.bias[x.c]))));
         dskip = __ffma2_rn(dy, u, dskip);
         dbias = __fadd2_rn(dbias, dd);
-        const uint32_t at = un.row(t + x.ng) + un.c0 + x.c;
-        const int64_t LD = p.L * p.D;
+        const uint32_t at = un.row(t + x.ng) + x.c;
+        void* out = again(sm.cta.du);
         if (p.du_part)
-            *reinterpret_cast<float2*>(p.du_part + un.kb * LD + at) = du;
+            *reinterpret_cast<float2*>(static_cast<float*>(out) + at) = du;
         else
-            *reinterpret_cast<raw*>(static_cast<io_t*>(p.g.du) + un.ub * LD + at) = P2::r(du);
-        *reinterpret_cast<raw*>(static_cast<io_t*>(p.g.ddelta) + un.kb * LD +
-                                (static_cast<uint32_t>(t + x.ng) * un.D + un.c0 + x.c)) = P2::r(dd);
+            *reinterpret_cast<raw*>(static_cast<io_t*>(out) + at) = P2::r(du);
+        *reinterpret_cast<raw*>(static_cast<io_t*>(again(sm.cta.ddelta)) +
+                                (static_cast<uint32_t>(t + x.ng) * un.D + x.c)) = P2::r(dd);
         if (p.z) {
             const float2 z = pair_at(&st.z[r][x.c]), sg = sigmoid_2(z);
-            const float2 y = __ffma2_rn(par.skip, u, sum(0));
+            const float2 y = __ffma2_rn(skip, u, sum(0));
             // silu'(z) = sg (1 + z (1 - sg))
             const float2 one = dup(1.f), rest = make_float2(1.f - sg.x, 1.f - sg.y);
             const float2 dz = __fmul2_rn(__fmul2_rn(pair_at(&st.dout[r][x.c]), y),
                                          __fmul2_rn(sg, __ffma2_rn(z, rest, one)));
+            out = again(sm.cta.dz);
             if (p.dz_part)
-                *reinterpret_cast<float2*>(p.dz_part + un.kb * LD + at) = dz;
+                *reinterpret_cast<float2*>(static_cast<float*>(out) + at) = dz;
             else
-                *reinterpret_cast<raw*>(static_cast<io_t*>(p.g.dz) + un.b * LD + at) = P2::r(dz);
+                *reinterpret_cast<raw*>(static_cast<io_t*>(out) + at) = P2::r(dz);
         }
     }
     // a lane adds the 8 channel pairs of one (step, tensor, 4 states); the lanes of the two
@@ -504,7 +542,7 @@ template <typename io_t>
 __device__ __forceinline__ void store_dbc(const BwdParams& p, const Unit& un, int t, GradSmem<io_t>& sm)
 {
     const int rows = min(un.t1 - t, kTL);
-    float* out = p.dbc + ((un.kb * un.ctiles + un.ctile) * p.L + t) * (2 * kNP);
+    float* out = again(sm.cta.dbc) + static_cast<int64_t>(t) * (2 * kNP);
     constexpr int kVec = 2 * kNP / 4;  // float4 of a step
     for (int j = threadIdx.x; j < rows * kVec; j += kBwdThreads) {
         const int r = j / kVec, q = (j / (kNP / 4)) & 1, n4 = j & (kNP / 4 - 1);
@@ -529,8 +567,8 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
     GradSmem<io_t>& sm = *reinterpret_cast<GradSmem<io_t>*>(raw_smem);
     const Unit un = unit_of(p);
     const Cell x = cell_of(un);
-    const Par par = load_par(p, un, x);
-    float2 A[4], g[4], dA[4], hstart[4];
+    fill_cta<io_t>(p, un, sm.cta);
+    float2 A[4], g[4], dA[4];
     load_A<PRECISE>(p, un, x, A);
     float2 dskip = dup(0.f), dbias = dup(0.f);
 
@@ -540,16 +578,19 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int n = 4 * x.ng + i;
-        hstart[i] = g[i] = dA[i] = dup(0.f);
-        if (x.valid && n < p.N) {
-            if (p.init)
-                hstart[i] = make_float2(p.init[cell + n], p.init[cell + p.N + n]);
-            if (p.dlast)
-                g[i] = make_float2(p.dlast[cell + n], p.dlast[cell + p.N + n]);
-        }
+        g[i] = dA[i] = dup(0.f);
+        if (p.dlast && x.valid && n < p.N)
+            g[i] = make_float2(p.dlast[cell + n], p.dlast[cell + p.N + n]);
     }
     if (SPLIT) {
-        float2 P[4], v[4];
+        float2 P[4], v[4], hstart[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = 4 * x.ng + i;
+            hstart[i] = dup(0.f);
+            if (p.init && x.valid && n < p.N)
+                hstart[i] = make_float2(p.init[cell + n], p.init[cell + p.N + n]);
+        }
         for (int s = 0; s < un.seg; ++s) {
             get4(seg_at(p.seg_p, p, un, s), kBwdThreads, P);
             get4(seg_at(p.seg_h, p, un, s), kBwdThreads, v);
@@ -557,6 +598,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
             for (int i = 0; i < 4; ++i)
                 hstart[i] = __ffma2_rn(P[i], hstart[i], v[i]);
         }
+        put4(&sm.hstart[0][threadIdx.x], kBwdThreads, hstart);
         for (int s = p.S - 1; s > un.seg; --s) {
             get4(seg_at(p.seg_p, p, un, s), kBwdThreads, P);
             get4(seg_at(p.seg_g, p, un, s), kBwdThreads, v);
@@ -570,11 +612,11 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
     int slice = (un.t1 - 1) / kT;  // of the sequence; segments start on slice borders
     // the next slice's checkpoint is on its way while this one is worked on
     float2 next[4], next_cum = dup(0.f);
-    get4(ckpt_at(p, un, slice), kBwdThreads, next);
+    get4(ckpt_at(un, sm.cta, slice), kBwdThreads, next);
     if (shift && x.valid)
-        next_cum = *cum_at(p, un, x, slice);
+        next_cum = *cum_at(un, sm.cta, x, slice);
     io_t bc[kBC][2];
-    issue<io_t>(p, un, un.t0 + (tiles - 1) * kTL, sm.st[(tiles - 1) & 1], true, bc);
+    issue<io_t>(p, un, sm.cta, un.t0 + (tiles - 1) * kTL, sm.st[(tiles - 1) & 1], true, bc);
     for (int it = tiles - 1; it >= 0; --it) {
         const int t = un.t0 + it * kTL;
         const Stage<io_t>& st = sm.st[it & 1];
@@ -582,10 +624,10 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
         __syncthreads();
         if (it + 1 < tiles)
             store_dbc(p, un, t + kTL, sm);
-        prepass(p, un, x, t, sm, st, par, true, bc);
+        prepass(p, un, x, t, sm, st, true, bc);
         __syncthreads();
         if (it > 0)
-            issue<io_t>(p, un, t - kTL, sm.st[(it - 1) & 1], true, bc);
+            issue<io_t>(p, un, sm.cta, t - kTL, sm.st[(it - 1) & 1], true, bc);
 
         for (int r0 = kTL - kT; r0 >= 0; r0 -= kT) {
             if (t + r0 >= un.t1)
@@ -596,37 +638,35 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
             for (int i = 0; i < 4; ++i)
                 h[0][i] = next[i];
             if (shift) {
+                float2 hstart[4];
+                get4(&sm.hstart[0][threadIdx.x], kBwdThreads, hstart);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 d = decay<PRECISE>(next_cum, A[i]);
-                    h[0][i] = __fadd2_rn(h[0][i], decayed<PRECISE>(d, hstart[i]));
-                }
+                for (int i = 0; i < 4; ++i)
+                    h[0][i] = __fadd2_rn(h[0][i], decayed<PRECISE>(decay<PRECISE>(next_cum, A[i]),
+                                                                   hstart[i]));
             }
             if (t + r0 > un.t0) {
                 --slice;
-                get4(ckpt_at(p, un, slice), kBwdThreads, next);
+                get4(ckpt_at(un, sm.cta, slice), kBwdThreads, next);
                 if (shift && x.valid)
-                    next_cum = *cum_at(p, un, x, slice);
+                    next_cum = *cum_at(un, sm.cta, x, slice);
             }
 #pragma unroll
             for (int r = 0; r < kT; ++r) {
-                float2 B[4], C[4], y;
+                float2 B[4];
                 load4(sm.B, r0 + r, x.ng, B);
                 const float2 dl = sm.scal[x.warp][r0 + r][0][x.cg];
                 const float2 w = sm.scal[x.warp][r0 + r][1][x.cg];
-                load4(sm.C, r0 + r, x.ng, C);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     a[r][i] = decay<PRECISE>(dl, A[i]);
                     h[r + 1][i] = decayed<PRECISE>(a[r][i], h[r][i], __fmul2_rn(w, B[i]));
-                    y = i ? __ffma2_rn(C[i], h[r + 1][i], y) : __fmul2_rn(C[i], h[r + 1][i]);
                 }
-                *reinterpret_cast<float2*>(&sm.part[x.warp][0][r][x.ng * kWC + 2 * x.cg]) = y;
             }
             // the reverse recurrence
 #pragma unroll
             for (int r = kT - 1; r >= 0; --r) {
-                float2 B[4], C[4], gB, gA;
+                float2 B[4], C[4], y, gB, gA;
                 load4(sm.B, r0 + r, x.ng, B);
                 load4(sm.C, r0 + r, x.ng, C);
                 const float2 dl = sm.scal[x.warp][r0 + r][0][x.cg];
@@ -635,9 +675,11 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
                 float dB[4], dC[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    g[i] = __ffma2_rn(dy, C[i], g[i]);
-                    const float2 c2 = __fmul2_rn(dy, h[r + 1][i]), b2 = __fmul2_rn(w, g[i]);
+                    y = i ? __ffma2_rn(C[i], h[r + 1][i], y) : __fmul2_rn(C[i], h[r + 1][i]);
+                    const float2 c2 = __fmul2_rn(dy, h[r + 1][i]);
                     dC[i] = c2.x + c2.y;
+                    g[i] = __ffma2_rn(dy, C[i], g[i]);
+                    const float2 b2 = __fmul2_rn(w, g[i]);
                     dB[i] = b2.x + b2.y;
                     gB = i ? __ffma2_rn(g[i], B[i], gB) : __fmul2_rn(g[i], B[i]);
                     g[i] = decayed<PRECISE>(a[r][i], g[i]);
@@ -645,6 +687,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
                     gA = i ? __ffma2_rn(q, A[i], gA) : __fmul2_rn(q, A[i]);
                     dA[i] = __ffma2_rn(q, dl, dA[i]);
                 }
+                *reinterpret_cast<float2*>(&sm.part[x.warp][0][r][x.ng * kWC + 2 * x.cg]) = y;
                 *reinterpret_cast<float2*>(&sm.part[x.warp][1][r][x.ng * kWC + 2 * x.cg]) = gB;
                 *reinterpret_cast<float2*>(&sm.part[x.warp][2][r][x.ng * kWC + 2 * x.cg]) = gA;
                 *reinterpret_cast<float4*>(&sm.dbc[x.warp][r][0][x.cg][4 * x.ng]) =
@@ -653,7 +696,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
                     make_float4(dC[0], dC[1], dC[2], dC[3]);
             }
             __syncwarp();
-            finish_slice(p, un, x, t + r0, r0, sm, st, par, dskip, dbias);
+            finish_slice(p, un, x, t + r0, r0, sm, st, dskip, dbias);
             __syncwarp();
         }
     }
