@@ -7,6 +7,7 @@
 #include <initializer_list>
 
 #include "so_internal.h"
+#include "ss_internal.h"
 
 namespace {
 
@@ -67,13 +68,35 @@ ss_status status_of(cudaError_t e) { return e == cudaSuccess ? SS_OK : SS_ERR_CU
 // ---------------------------------------------------------------- gated linear recurrence
 
 struct RecPlan {
-    int S;
+    int cluster, S;
     int64_t seg_len;
-    size_t off_carry, off_dbias, bytes;
+    size_t off_maps, bytes;
 };
 
-// Enough segments for about 1024 threads (of two channels each) on each of the 148 SMs of a B200,
-// but none shorter than 32 steps: below that the carries cost more than the parallelism gives.
+// CTAs in the cluster of a column of 64 channels.  A B200 runs about three of the recurrence's CTAs
+// on each of its 148 SMs best, so a launch takes as long as its whole waves of 444: the cluster is
+// the size that fills them best, less 2% for each CTA that has to be heard.  Even sizes only: 3 and 5
+// measured slower than their neighbours (8 x 2048 x 1536: 45 us at 1, 36.9 at 2, 45 at 3 and 4).
+constexpr int64_t kRecSlots = 3 * 148;
+
+int rec_cluster(int64_t columns, int64_t tiles)
+{
+    int best = 1;
+    double most = 0.;
+    for (int cs : {1, 2, 4, 6, 8}) {
+        if (cs > so::kRecMostCluster || cs > tiles)
+            break;
+        const double waves = static_cast<double>(columns) * cs / kRecSlots;
+        const double full = waves / static_cast<double>(ceil_div(columns * cs, kRecSlots));
+        const double score = full * (1. - 0.02 * (cs - 1));
+        if (score > most) {
+            most = score;
+            best = cs;
+        }
+    }
+    return best;
+}
+
 ss_status plan_recurrence(const ss_shape* s, const ss_recurrence_opts* o, bool backward, RecPlan* pl)
 {
     ss_status st = check_shape(s);
@@ -87,24 +110,31 @@ ss_status plan_recurrence(const ss_shape* s, const ss_recurrence_opts* o, bool b
         return SS_ERR_UNSUPPORTED;
     if (o->dir != SS_DIR_FWD && o->dir != SS_DIR_REV)
         return SS_ERR_DIRMAP;
-    const int64_t threads = s->batch * s->dim / 2;
-    int64_t S = threads > 0 ? ceil_div(148 * 1024, threads) : 1;
-    if (S > s->seqlen / 32)
-        S = s->seqlen / 32;
-    if (S > kMaxSegments)
-        S = kMaxSegments;
-    if (S < 1)
+    const int64_t columns = s->batch * ceil_div(s->dim, 64);
+    const int64_t tiles = ceil_div(s->seqlen, so::recurrence_tile(s->io_dtype, backward));
+    pl->cluster = columns > 0 && tiles > 0 ? rec_cluster(columns, tiles) : 1;
+    // Segments only where whole clusters fill less than half of the GPU and a column has rounds to
+    // share out: four at least for each segment.
+    const int64_t round = static_cast<int64_t>(so::recurrence_tile(s->io_dtype, backward)) * pl->cluster;
+    const int64_t rounds = ceil_div(s->seqlen, round);
+    int64_t S = 1;
+    if (columns > 0 && pl->cluster == so::kRecMostCluster)
+        S = kRecSlots / (columns * pl->cluster);
+    if (S > rounds / 4)
+        S = rounds / 4;
+    if (S < 2)
         S = 1;
-    pl->seg_len = s->seqlen > 0 ? ceil_div(s->seqlen, S) : 1;
-    pl->S = s->seqlen > 0 ? static_cast<int>(ceil_div(s->seqlen, pl->seg_len)) : 1;
-    if (ceil_div(s->dim, 64) * s->batch * pl->S > kMaxI32)
+    pl->seg_len = ceil_div(rounds > 0 ? rounds : 1, S) * round;
+    pl->S = static_cast<int>(s->seqlen > 0 ? ceil_div(s->seqlen, pl->seg_len) : 1);
+    if (columns * pl->S * pl->cluster > kMaxI32)
         return SS_ERR_SHAPE;
-    const size_t cells = static_cast<size_t>(s->batch) * s->dim * pl->S;
-    pl->off_carry = 0;
-    pl->bytes = pl->S > 1 ? align256(cells * sizeof(float2)) : 0;
-    pl->off_dbias = pl->bytes;
+    pl->bytes = 0;
     if (backward && o->form == SS_GATE_SIGMOID)
-        pl->bytes += align256(cells * sizeof(float));
+        pl->bytes = align256(static_cast<size_t>(s->batch) * s->dim * pl->S * pl->cluster *
+                             sizeof(float));
+    pl->off_maps = pl->bytes;
+    if (pl->S > 1)
+        pl->bytes += static_cast<size_t>(columns) * pl->S * 32 * sizeof(float4);
     return SS_OK;
 }
 
@@ -284,15 +314,21 @@ ss_status gated_recurrence_fwd(const ss_shape* shape, const ss_recurrence_opts* 
     p.init = initial_state;
     p.out = out;
     p.last = last_state;
-    p.carry = reinterpret_cast<float2*>(static_cast<unsigned char*>(workspace) + pl.off_carry);
     p.batch = b;
     p.L = L;
     p.D = D;
+    p.cluster = pl.cluster;
     p.S = pl.S;
-    p.seg_len = pl.seg_len;
+    p.seg_len = static_cast<int32_t>(pl.seg_len < L ? pl.seg_len : L);
+    p.seg_maps = pl.S > 1 ? reinterpret_cast<float4*>(static_cast<unsigned char*>(workspace) +
+                                                      pl.off_maps)
+                          : nullptr;
     p.form = opts->form;
     p.complement = opts->complement != 0;
     p.reverse = opts->dir == SS_DIR_REV;
+    p.status = ss::status_word();
+    if (!p.status)
+        return SS_ERR_CUDA;
     return status_of(so::launch_recurrence(p, shape->io_dtype, false, strm));
 }
 
@@ -333,7 +369,6 @@ ss_status gated_recurrence_bwd(const ss_shape* shape, const ss_recurrence_opts* 
                             : cudaMemsetAsync(dinitial_state, 0, n, strm);
         return status_of(e);
     }
-    unsigned char* ws = static_cast<unsigned char*>(workspace);
     so::RecParams p;
     std::memset(&p, 0, sizeof(p));
     p.x = x;
@@ -347,16 +382,22 @@ ss_status gated_recurrence_bwd(const ss_shape* shape, const ss_recurrence_opts* 
     p.dgate = dgate;
     p.last = dinitial_state;
     p.dbias = dgate_bias;
-    p.dbias_part = dgate_bias ? reinterpret_cast<float*>(ws + pl.off_dbias) : nullptr;
-    p.carry = reinterpret_cast<float2*>(ws + pl.off_carry);
+    p.dbias_part = dgate_bias ? static_cast<float*>(workspace) : nullptr;
     p.batch = b;
     p.L = L;
     p.D = D;
+    p.cluster = pl.cluster;
     p.S = pl.S;
-    p.seg_len = pl.seg_len;
+    p.seg_len = static_cast<int32_t>(pl.seg_len < L ? pl.seg_len : L);
+    p.seg_maps = pl.S > 1 ? reinterpret_cast<float4*>(static_cast<unsigned char*>(workspace) +
+                                                      pl.off_maps)
+                          : nullptr;
     p.form = opts->form;
     p.complement = opts->complement != 0;
     p.reverse = opts->dir == SS_DIR_REV;
+    p.status = ss::status_word();
+    if (!p.status)
+        return SS_ERR_CUDA;
     return status_of(so::launch_recurrence(p, shape->io_dtype, true, strm));
 }
 

@@ -24,15 +24,23 @@ struct RecParams {
     void* out;             // forward: [batch, L, D]; backward: dx
     void* dgate;           // backward
     float* last;           // forward: last state or null; backward: dinitial or null
-    float* dbias_part;     // backward: [batch * S, D] partial sums of ds, or null
+    float* dbias_part;     // backward: [batch * S * cluster, D] partial sums of ds, or null
     float* dbias;          // backward: [D] or null
-    float2* carry;         // [batch, S, D] aggregates of the segments (S > 1)
-    int64_t batch, L, D, seg_len;
-    int32_t S;
+    int64_t batch, L, D;
+    float4* seg_maps;      // [columns, S, 32] maps of the segments of a split column (S > 1)
+    int32_t cluster;       // CTAs that walk one column of 64 channels together
+    int32_t S, seg_len;    // segments of a column, their steps (whole rounds of the cluster)
+    int32_t aggregate;     // set by the launcher
     int32_t form, complement, reverse;
+    unsigned int* status;  // the device error word, or'ed by waits that gave up
 };
 
+constexpr int kRecMostCluster = 8;
+
 cudaError_t launch_recurrence(const RecParams& p, int io_dtype, bool backward, cudaStream_t st);
+
+// Steps of a CTA's tile.
+int recurrence_tile(int io_dtype, bool backward);
 
 // ---------------------------------------------------------------- gradient of the scan
 
