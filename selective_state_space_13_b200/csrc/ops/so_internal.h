@@ -82,6 +82,7 @@ struct StepParams {
     void* out;
     int64_t batch, D, num_slots;
     int32_t N, softplus, conv_width;
+    int32_t rows;  // rows of a CTA, set by the launcher
 };
 
 cudaError_t launch_step(const StepParams& p, int io_dtype, cudaStream_t st);

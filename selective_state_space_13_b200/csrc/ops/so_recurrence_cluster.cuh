@@ -62,8 +62,8 @@ template <int FORM, bool ACCURATE>
 __device__ __forceinline__ float2 decay_minus_one(float2 gate, float2 bias2)
 {
     const float2 log2e = make_float2(kLog2e, kLog2e), minus = make_float2(-1.f, -1.f);
-    const float2 s = FORM == SS_GATE_SIGMOID ? __ffma2_rn(gate, log2e, bias2)
-                                             : __fmul2_rn(gate, log2e);
+    const float2 shift = make_float2(kDecayShift, kDecayShift);
+    const float2 s = __ffma2_rn(gate, log2e, FORM == SS_GATE_SIGMOID ? bias2 : shift);
     const float2 e = make_float2(ex2(s.x), ex2(s.y));
     if (FORM == SS_GATE_SIGMOID) {
         const float2 q = __ffma2_rn(e, minus, minus);

@@ -279,8 +279,7 @@ __device__ __forceinline__ void load_A(const BwdParams& p, const Unit& un, const
 // The decay of a step: Abar, or Abar - 1 with PRECISE.
 template <bool PRECISE> __device__ __forceinline__ float2 decay(float2 delta, float2 A)
 {
-    const float2 x = __fmul2_rn(delta, A);
-    return PRECISE ? expm1_2(x) : ex2_2(x);
+    return PRECISE ? expm1_2(__fmul2_rn(delta, A)) : ex2_2(__ffma2_rn(delta, A, dup(kDecayShift)));
 }
 
 // Abar v + w with that decay.

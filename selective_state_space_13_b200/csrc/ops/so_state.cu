@@ -1,9 +1,10 @@
 // Parking of recurrent states in 8 or 4 bits and reading them back: N states of a channel share
-// one fp32 scale.  Both directions move bytes and nothing else, so HBM bounds them.  As in the
-// step, LPC lanes share a channel with 16-byte state accesses where N is a multiple of 4, and
-// other N take one lane per channel.
+// one fp32 scale.  Both directions move bytes and nothing else, so HBM bounds them.  A warp has 32
+// channels of a row; where N is a multiple of 4, LPC lanes share a channel with 16-byte state
+// accesses in LPC passes (as in the step), and what belongs to a whole channel -- the scale, and in
+// the load its codes, 16 bytes for 16 states -- is one lane's; other N take one lane per channel.
 //
-// round(h q / amax) is what fp32 arithmetic gives wherever its error (below 2^-22 q) cannot move
+// round(h q / amax) is what fp32 arithmetic gives wherever its error (below 2^-21 q) cannot move
 // the value across the border between two codes; next to a border the quotient is taken again in
 // fp64, where h q is exact and the correctly rounded quotient of two fp32 numbers lies on a border
 // only if the true one does.  So the codes are those of exact arithmetic.
@@ -13,163 +14,247 @@ namespace so {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
 
-__device__ __forceinline__ int code_of(float h, float amax, float inv, int q)
+// The codes of NS states, as bytes; amax is finite and not zero.
+template <int NS>
+__device__ __forceinline__ void codes_of(const float* h, float amax, int q, uint32_t* code)
 {
-    const float v = h * inv;
-    const float r = rintf(v);
-    // |v - r| is 1/2 on a border; q 2^-22 < 1e-4.  inv is 0 where q / amax leaves the fp32 range.
-    if (inv != 0.f && fabsf(fabsf(v - r) - 0.5f) > 1e-4f)
-        return static_cast<int>(r);
-    return static_cast<int>(rint(static_cast<double>(h) * q / static_cast<double>(amax)));
+    // inv is 0 or infinite where q / amax leaves the fp32 range: those go the long way
+    const float inv = static_cast<float>(q) * rcp(amax);
+    const float magic = 12582912.f;  // 1.5 * 2^23: adding it leaves the rounded integer in the low bits
+    float off = inv > 0.f && inv < 1e30f ? 0.f : 1.f;
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+        const float v = h[n] * inv;
+        const float t = v + magic;
+        off = fmaxf(off, fabsf(v - (t - magic)));  // 1/2 on a border
+        code[n] = __float_as_uint(t);
+    }
+    if (off > 0.5f - 1e-4f) {
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+            code[n] = static_cast<uint32_t>(
+                static_cast<int>(rint(static_cast<double>(h[n]) * q / static_cast<double>(amax))));
+    }
 }
 
-template <int LPC, bool VEC, int BITS>
+// Four codes in one unit: 4 bytes, or 4 nibbles with the even states in the low halves.
+template <int BITS> struct Unit;
+template <> struct Unit<8> {
+    using type = uint32_t;
+    static __device__ __forceinline__ type pack(const uint32_t* c)
+    {
+        return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    }
+    static __device__ __forceinline__ int get(type v, int n)
+    {
+        return static_cast<int8_t>(v >> (8 * n));
+    }
+};
+template <> struct Unit<4> {
+    using type = uint16_t;
+    static __device__ __forceinline__ type pack(const uint32_t* c)
+    {
+        return static_cast<type>((c[0] & 15) | (c[1] & 15) << 4 | (c[2] & 15) << 8 | c[3] << 12);
+    }
+    static __device__ __forceinline__ int get(type v, int n)
+    {
+        return static_cast<int>(static_cast<uint32_t>(v) << (28 - 4 * n)) >> 28;
+    }
+};
+
+// The row of a CTA: its slots in both pools (false: skipped, the same for the whole CTA), and the
+// first channel of the warp.
+struct Place {
+    int64_t row, src, dst, d0;
+
+    __device__ __forceinline__ bool set(const StateParams& p)
+    {
+        const int64_t tiles = (p.D + kThreads - 1) / kThreads;
+        row = blockIdx.x / tiles;
+        d0 = (blockIdx.x % tiles) * kThreads + (threadIdx.x >> 5) * 32;
+        src = p.src ? p.src[row] : row;
+        dst = p.dst ? p.dst[row] : row;
+        return src >= 0 && src < p.src_slots && dst >= 0 && dst < p.dst_slots;
+    }
+};
+
+__device__ __forceinline__ float scale_of(unsigned top, int q)
+{
+    return top < 0x7f800000u ? __fdiv_rn(__uint_as_float(top), static_cast<float>(q))
+                             : __uint_as_float(0x7fc00000u);
+}
+
+template <int LPC, int BITS>
 __global__ void __launch_bounds__(kThreads) store_kernel(const StateParams p)
 {
-    constexpr int CH = kThreads / LPC, NS = VEC ? 4 : SS_MAX_DSTATE, Q = BITS == 8 ? 127 : 7;
-    const int64_t tiles = (p.D + CH - 1) / CH;
-    const int64_t row = blockIdx.x / tiles;
-    const int64_t src = p.src ? p.src[row] : row, dst = p.dst ? p.dst[row] : row;
-    if (src < 0 || src >= p.src_slots || dst < 0 || dst >= p.dst_slots)
-        return;  // the same for the whole CTA
-    const int64_t d = (blockIdx.x % tiles) * CH + threadIdx.x / LPC;
-    const int n0 = VEC ? 4 * (threadIdx.x % LPC) : 0;
-    const int nn = VEC ? 4 : p.N;
-    const bool active = d < p.D, holds = active && n0 < p.N;
-    const float* state = p.state_in + (src * p.D + d) * p.N + n0;
-    float h[NS];
-    if (VEC) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (holds)
-            v = *reinterpret_cast<const float4*>(state);
-        h[0] = v.x, h[1] = v.y, h[2] = v.z, h[3] = v.w;
-    } else {
-#pragma unroll
-        for (int n = 0; n < NS; ++n)
-            h[n] = holds && n < nn ? state[n] : 0.f;
-    }
-    if (p.dst && slot_taken(p.dst, row, static_cast<int32_t>(dst), p.src, p.src_slots))
+    constexpr int Q = BITS == 8 ? 127 : 7, CP = 32 / LPC;
+    using unit_t = typename Unit<BITS>::type;
+    Place at;
+    if (!at.set(p))
         return;
-
-    // the largest magnitude by its bits, so that NaN and infinity stand above every number
-    unsigned top = 0;
+    const int lane = threadIdx.x & 31, ng = lane % LPC;
+    float4 h[LPC];
 #pragma unroll
-    for (int n = 0; n < NS; ++n)
-        top = max(top, __float_as_uint(h[n]) & 0x7fffffffu);
-#pragma unroll
-    for (int m = LPC / 2; m > 0; m /= 2)
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
-    const float amax = __uint_as_float(top);
-    const bool fine = top < 0x7f800000u;
-    const float scale = fine ? __fdiv_rn(amax, static_cast<float>(Q)) : __uint_as_float(0x7fc00000u);
-    const float inv = amax > 1e-30f ? __fdiv_rn(static_cast<float>(Q), amax) : 0.f;
-    int code[NS];
-#pragma unroll
-    for (int n = 0; n < NS; ++n)
-        code[n] = fine && top ? code_of(h[n], amax, inv, Q) : 0;
-    if (!holds)
-        return;
-    if (VEC ? threadIdx.x % LPC == 0 : true)
-        p.scales[dst * p.D + d] = scale;
-    if (BITS == 8) {
-        uint8_t* o = p.codes + (dst * p.D + d) * p.N + n0;
-        if (VEC) {
-            *reinterpret_cast<uchar4*>(o) = make_uchar4(code[0], code[1], code[2], code[3]);
-        } else {
-#pragma unroll
-            for (int n = 0; n < NS; ++n)
-                if (n < nn)
-                    o[n] = static_cast<uint8_t>(code[n]);
-        }
-    } else {
-        uint8_t* o = p.codes + (dst * p.D + d) * ((p.N + 1) / 2) + n0 / 2;
-#pragma unroll
-        for (int n = 0; n < NS; n += 2)
-            if (n < nn)
-                o[n / 2] = static_cast<uint8_t>((code[n] & 15) | (code[n + 1] << 4));
+    for (int s = 0; s < LPC; ++s) {
+        const int64_t d = at.d0 + s * CP + lane / LPC;
+        h[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (d < p.D && 4 * ng < p.N)
+            h[s] = *reinterpret_cast<const float4*>(p.state_in + (at.src * p.D + d) * p.N + 4 * ng);
     }
+    if (p.dst && slot_taken(p.dst, at.row, static_cast<int32_t>(at.dst), p.src, p.src_slots))
+        return;
+    unsigned mine = 0;  // the largest magnitude of channel d0 + lane
+#pragma unroll
+    for (int s = 0; s < LPC; ++s) {
+        const float v[4] = {h[s].x, h[s].y, h[s].z, h[s].w};
+        // by their bits, so that NaN and infinity stand above every number
+        unsigned top = 0;
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            top = max(top, __float_as_uint(v[n]) & 0x7fffffffu);
+#pragma unroll
+        for (int m = LPC / 2; m > 0; m /= 2)
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+        const unsigned back = LPC > 1 ? __shfl_sync(0xffffffffu, top, (lane % CP) * LPC) : top;
+        mine = lane / CP == s ? back : mine;
+        uint32_t code[4] = {0, 0, 0, 0};
+        if (top - 1 < 0x7f7fffffu)  // neither zero nor infinite nor NaN
+            codes_of<4>(v, __uint_as_float(top), Q, code);
+        const int64_t d = at.d0 + s * CP + lane / LPC;
+        if (d < p.D && 4 * ng < p.N)
+            reinterpret_cast<unit_t*>(p.codes)[(at.dst * p.D + d) * (p.N / 4) + ng] =
+                Unit<BITS>::pack(code);
+    }
+    if (at.d0 + lane < p.D)
+        p.scales[at.dst * p.D + at.d0 + lane] = scale_of(mine, Q);
 }
 
-template <int LPC, bool VEC, int BITS>
+template <int LPC, int BITS>
 __global__ void __launch_bounds__(kThreads) load_kernel(const StateParams p)
 {
-    constexpr int CH = kThreads / LPC, NS = VEC ? 4 : SS_MAX_DSTATE;
-    const int64_t tiles = (p.D + CH - 1) / CH;
-    const int64_t row = blockIdx.x / tiles;
-    const int64_t src = p.src ? p.src[row] : row, dst = p.dst ? p.dst[row] : row;
-    if (src < 0 || src >= p.src_slots || dst < 0 || dst >= p.dst_slots)
+    constexpr int CP = 32 / LPC;
+    using unit_t = typename Unit<BITS>::type;
+    struct alignas(sizeof(unit_t) * LPC) Codes {  // of a channel (N = 12: the fourth is unused)
+        unit_t v[LPC];
+    };
+    __shared__ Codes s_codes[kWarps][32];
+    Place at;
+    if (!at.set(p))
         return;
-    const int64_t d = (blockIdx.x % tiles) * CH + threadIdx.x / LPC;
-    const int n0 = VEC ? 4 * (threadIdx.x % LPC) : 0;
-    const int nn = VEC ? 4 : p.N;
-    const bool holds = d < p.D && n0 < p.N;
-    int code[NS];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ng = lane % LPC;
+    const int64_t d = at.d0 + lane;
+    const int units = p.N / 4;
     float scale = 0.f;
-#pragma unroll
-    for (int n = 0; n < NS; ++n)
-        code[n] = 0;
-    if (holds) {
-        scale = p.scales[src * p.D + d];
-        if (BITS == 8) {
-            const int8_t* c = reinterpret_cast<const int8_t*>(p.codes) + (src * p.D + d) * p.N + n0;
-            if (VEC) {
-                const char4 v = *reinterpret_cast<const char4*>(c);
-                code[0] = v.x, code[1] = v.y, code[2] = v.z, code[3] = v.w;
-            } else {
-#pragma unroll
-                for (int n = 0; n < NS; ++n)
-                    if (n < nn)
-                        code[n] = c[n];
-            }
+    Codes c = {};
+    if (d < p.D) {
+        const unit_t* from = reinterpret_cast<const unit_t*>(p.codes) + (at.src * p.D + d) * units;
+        scale = p.scales[at.src * p.D + d];
+        if (units == LPC) {
+            c = *reinterpret_cast<const Codes*>(from);
         } else {
-            const int8_t* c = reinterpret_cast<const int8_t*>(p.codes) +
-                              (src * p.D + d) * ((p.N + 1) / 2) + n0 / 2;
 #pragma unroll
-            for (int n = 0; n < NS; n += 2)
-                if (n < nn) {
-                    const int v = c[n / 2];
-                    code[n] = static_cast<int8_t>(v << 4) >> 4;
-                    code[n + 1] = v >> 4;
-                }
+            for (int i = 0; i < LPC; ++i)
+                if (i < units)
+                    c.v[i] = from[i];
         }
     }
-    if (p.dst && slot_taken(p.dst, row, static_cast<int32_t>(dst), p.src, p.src_slots))
+    if (p.dst && slot_taken(p.dst, at.row, static_cast<int32_t>(at.dst), p.src, p.src_slots))
         return;
-    if (!holds)
-        return;
-    float* state = p.state_out + (dst * p.D + d) * p.N + n0;
-    if (VEC) {
-        *reinterpret_cast<float4*>(state) =
-            make_float4(code[0] * scale, code[1] * scale, code[2] * scale, code[3] * scale);
-    } else {
+    s_codes[warp][lane] = c;
+    __syncwarp();
 #pragma unroll
-        for (int n = 0; n < NS; ++n)
-            if (n < nn)
-                state[n] = code[n] * scale;
+    for (int s = 0; s < LPC; ++s) {
+        const int ch = s * CP + lane / LPC;
+        const float sc = __shfl_sync(0xffffffffu, scale, ch);
+        const unit_t v = s_codes[warp][ch].v[ng];
+        if (at.d0 + ch < p.D && 4 * ng < p.N)
+            *reinterpret_cast<float4*>(p.state_out + (at.dst * p.D + at.d0 + ch) * p.N + 4 * ng) =
+                make_float4(Unit<BITS>::get(v, 0) * sc, Unit<BITS>::get(v, 1) * sc,
+                            Unit<BITS>::get(v, 2) * sc, Unit<BITS>::get(v, 3) * sc);
     }
 }
 
-template <int LPC, bool VEC, int BITS>
+// Any other N: one lane per channel.
+template <int BITS>
+__global__ void __launch_bounds__(kThreads) store_any_kernel(const StateParams p)
+{
+    constexpr int Q = BITS == 8 ? 127 : 7, NS = SS_MAX_DSTATE;
+    Place at;
+    if (!at.set(p))
+        return;
+    const int64_t d = at.d0 + (threadIdx.x & 31);
+    if (p.dst && slot_taken(p.dst, at.row, static_cast<int32_t>(at.dst), p.src, p.src_slots))
+        return;
+    if (d >= p.D)
+        return;
+    const float* state = p.state_in + (at.src * p.D + d) * p.N;
+    float h[NS];
+    unsigned top = 0;
+    uint32_t code[NS];
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+        h[n] = n < p.N ? state[n] : 0.f;
+        top = max(top, __float_as_uint(h[n]) & 0x7fffffffu);
+        code[n] = 0;
+    }
+    if (top - 1 < 0x7f7fffffu)
+        codes_of<NS>(h, __uint_as_float(top), Q, code);
+    p.scales[at.dst * p.D + d] = scale_of(top, Q);
+    const int bytes = BITS == 8 ? p.N : (p.N + 1) / 2;
+    uint8_t* o = p.codes + (at.dst * p.D + d) * bytes;
+#pragma unroll
+    for (int i = 0; i < NS * BITS / 8; ++i)
+        if (i < bytes)
+            o[i] = static_cast<uint8_t>(BITS == 8 ? code[i]
+                                                  : (code[2 * i % NS] & 15) | code[(2 * i + 1) % NS] << 4);
+}
+
+template <int BITS>
+__global__ void __launch_bounds__(kThreads) load_any_kernel(const StateParams p)
+{
+    Place at;
+    if (!at.set(p))
+        return;
+    const int64_t d = at.d0 + (threadIdx.x & 31);
+    if (p.dst && slot_taken(p.dst, at.row, static_cast<int32_t>(at.dst), p.src, p.src_slots))
+        return;
+    if (d >= p.D)
+        return;
+    const int bytes = BITS == 8 ? p.N : (p.N + 1) / 2;
+    const uint8_t* c = p.codes + (at.src * p.D + d) * bytes;
+    const float scale = p.scales[at.src * p.D + d];
+    float* state = p.state_out + (at.dst * p.D + d) * p.N;
+#pragma unroll
+    for (int n = 0; n < SS_MAX_DSTATE; ++n)
+        if (n < p.N) {
+            const uint32_t v = c[n * BITS / 8] >> (BITS == 4 ? 4 * (n & 1) : 0);
+            state[n] = (static_cast<int>(v << (32 - BITS)) >> (32 - BITS)) * scale;
+        }
+}
+
+template <int LPC, int BITS>
 cudaError_t launch(const StateParams& p, bool load, cudaStream_t st)
 {
-    constexpr int CH = kThreads / LPC;
-    const unsigned blocks = static_cast<unsigned>((p.D + CH - 1) / CH * p.rows);
-    if (load)
-        load_kernel<LPC, VEC, BITS><<<blocks, kThreads, 0, st>>>(p);
+    const unsigned blocks = static_cast<unsigned>((p.D + kThreads - 1) / kThreads * p.rows);
+    if (LPC == 0)
+        load ? load_any_kernel<BITS><<<blocks, kThreads, 0, st>>>(p)
+             : store_any_kernel<BITS><<<blocks, kThreads, 0, st>>>(p);
     else
-        store_kernel<LPC, VEC, BITS><<<blocks, kThreads, 0, st>>>(p);
+        load ? load_kernel<LPC ? LPC : 1, BITS><<<blocks, kThreads, 0, st>>>(p)
+             : store_kernel<LPC ? LPC : 1, BITS><<<blocks, kThreads, 0, st>>>(p);
     return cudaGetLastError();
 }
 
 template <int BITS> cudaError_t launch_n(const StateParams& p, bool load, cudaStream_t st)
 {
     if (p.N % 4)
-        return launch<1, false, BITS>(p, load, st);
-    return p.N == 4 ? launch<1, true, BITS>(p, load, st)
-         : p.N == 8 ? launch<2, true, BITS>(p, load, st)
-                    : launch<4, true, BITS>(p, load, st);
+        return launch<0, BITS>(p, load, st);
+    return p.N == 4 ? launch<1, BITS>(p, load, st)
+         : p.N == 8 ? launch<2, BITS>(p, load, st)
+                    : launch<4, BITS>(p, load, st);
 }
 
 }  // namespace

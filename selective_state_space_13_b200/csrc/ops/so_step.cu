@@ -1,125 +1,239 @@
 // The selective scan's step for one token per row, on a pool of states that is updated in place.
 //
 // A step reads and writes 4 N bytes of state per channel and computes 7 operations per state, so
-// HBM bounds it for many rows and latency for one.  Four states make one 16-byte access: LPC lanes
-// share a channel (N = 4: 1, N = 8: 2, N = 12 and 16: 4), so a warp's state accesses are
-// contiguous; other N take one lane per channel and 4-byte accesses, whose lines the next states
-// of the same channels find in L1.
+// HBM bounds it for many rows and latency for one.  A warp has 32 channels of a row.  The
+// elementwise work (convolution, softplus, gates) runs with one channel a lane.  For the states,
+// LPC lanes share a channel with 16-byte accesses (N = 4: 1, N = 8: 2, N = 12 and 16: 4), in LPC
+// passes over 32 / LPC channels each, so that every access of a warp is contiguous; Delta and
+// Delta u come to the lanes of a channel by shuffle and y goes back the same way.  (With the
+// elementwise work done by every lane of a channel the kernel issued 293 instructions for 8 channels
+// and was bound by that: 72 us for 256 rows x 5120 channels x 16 states.)  Other N take one lane per
+// channel and 4-byte accesses, whose lines the next states of the same channels find in L1.  A CTA
+// keeps its channels' parameters (A alone is as long as a row's state) for up to kRows rows, one
+// row's loads ahead of the arithmetic.
 #include "so_device.cuh"
 
 namespace so {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kRows = 8;  // rows of a CTA at most
+
+// What a row brings to a lane: the states of its cells, B and C of its state group, and the inputs
+// of its channel.
+template <typename io_t, int LPC, int NS> struct Row {
+    float h[LPC][NS];
+    alignas(8) io_t B[NS], C[NS];
+    io_t u, delta, z, seen[SS_MAX_CONV_WIDTH - 1];
+};
 
 template <typename io_t, int LPC, bool VEC>
 __global__ void __launch_bounds__(kThreads) step_kernel(const StepParams p)
 {
-    constexpr int CH = kThreads / LPC;        // channels of a CTA
-    constexpr int NS = VEC ? 4 : SS_MAX_DSTATE;  // states a lane may hold
-    const int64_t tiles = (p.D + CH - 1) / CH;
-    const int64_t row = blockIdx.x / tiles;
-    const int64_t slot = p.slots ? p.slots[row] : row;
-    if (slot < 0 || slot >= p.num_slots)
-        return;  // the same for the whole CTA
-    const int64_t d = (blockIdx.x % tiles) * CH + threadIdx.x / LPC;
-    const int n0 = VEC ? 4 * (threadIdx.x % LPC) : 0;
+    constexpr int NS = VEC ? 4 : SS_MAX_DSTATE;  // states of a cell
+    constexpr int CP = 32 / LPC;                 // channels of a pass
+    __shared__ int s_slot[kRows];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tiles = static_cast<int>((p.D + kThreads - 1) / kThreads);
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x / tiles) * p.rows;
+    const int rows = static_cast<int>(p.batch - row0 < p.rows ? p.batch - row0 : p.rows);
+    const int64_t d0 = static_cast<int64_t>(blockIdx.x % tiles) * kThreads + warp * 32;
+    const int64_t d = d0 + lane;             // the lane's channel in elementwise work
+    const int n0 = VEC ? 4 * (lane % LPC) : 0;
     const int nn = VEC ? 4 : p.N;
-    const bool active = d < p.D, holds = active && n0 < p.N;
-    float* state = p.state + (slot * p.D + d) * p.N + n0;
-    float h[NS], A[NS];
-    if (VEC) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f), a = v;
-        if (holds) {
-            v = *reinterpret_cast<const float4*>(state);
-            a = make_float4(p.A[d * p.N + n0], p.A[d * p.N + n0 + 1], p.A[d * p.N + n0 + 2],
-                            p.A[d * p.N + n0 + 3]);
-        }
-        h[0] = v.x, h[1] = v.y, h[2] = v.z, h[3] = v.w;
-        A[0] = a.x, A[1] = a.y, A[2] = a.z, A[3] = a.w;
-    } else {
-#pragma unroll
-        for (int n = 0; n < NS; ++n) {
-            h[n] = holds && n < nn ? state[n] : 0.f;
-            A[n] = holds && n < nn ? p.A[d * p.N + n] : 0.f;
-        }
-    }
-    // the inputs before this token; every lane of a channel reads them before one shifts them
+    const bool active = d < p.D;
     const int width = p.conv_width;
-    io_t* win = static_cast<io_t*>(p.conv_state) + slot * (width - 1) * p.D + d;
-    io_t seen[SS_MAX_CONV_WIDTH - 1];
-#pragma unroll
-    for (int j = 0; j < SS_MAX_CONV_WIDTH - 1; ++j)
-        if (active && j < width - 1)
-            seen[j] = win[j * p.D];
-    // the rows before this one decide whether the slot is this row's
-    if (p.slots && slot_taken(p.slots, row, static_cast<int32_t>(slot), nullptr, p.batch))
-        return;
-    __syncwarp();
 
-    float u = 0.f, delta = 0.f, y = 0.f;
+    // the rows' slots, -1 for padding: a slot outside the pool, or one that an earlier row takes
+    for (int r = warp; r < rows; r += kWarps) {
+        const int64_t row = row0 + r;
+        int slot = static_cast<int>(row);
+        if (p.slots) {
+            slot = __ldg(p.slots + row);
+            int hit = slot < 0 || slot >= p.num_slots;
+            for (int64_t i = lane; i < row; i += 32)
+                hit |= __ldg(p.slots + i) == slot;
+            if (__any_sync(0xffffffffu, hit))
+                slot = -1;
+        }
+        if (lane == 0)
+            s_slot[r] = slot;
+    }
+    // the parameters of the lane's cells and of its channel
+    float A[LPC][NS], cw[SS_MAX_CONV_WIDTH], cb = 0.f, skip = 0.f, bias = 0.f;
+    bool holds[LPC];
+#pragma unroll
+    for (int s = 0; s < LPC; ++s) {
+        const int64_t c = d0 + s * CP + lane / LPC;
+        holds[s] = c < p.D && n0 < p.N;
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+            A[s][n] = holds[s] && n < nn ? p.A[c * p.N + n0 + n] * kLog2e : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < SS_MAX_CONV_WIDTH; ++j)
+        cw[j] = active && j < width ? p.conv_w[d * width + j] : 0.f;
     if (active) {
-        const io_t* gu = static_cast<const io_t*>(p.u) + row * p.D + d;
-        u = ld1(gu);
-        if (p.conv_w) {
-            const float* cw = p.conv_w + d * width;
-            float c = p.conv_b ? p.conv_b[d] : 0.f;
+        cb = p.conv_b ? p.conv_b[d] : 0.f;
+        skip = p.Dskip ? p.Dskip[d] : 0.f;
+        bias = p.bias ? p.bias[d] : 0.f;
+    }
+    __syncthreads();
+
+    auto state_at = [&](int slot, int s) {
+        return p.state + (static_cast<int64_t>(slot) * p.D + d0 + s * CP + lane / LPC) * p.N + n0;
+    };
+    auto window_at = [&](int slot) {
+        return static_cast<io_t*>(p.conv_state) + static_cast<int64_t>(slot) * (width - 1) * p.D + d;
+    };
+    auto load = [&](int r, Row<io_t, LPC, NS>& x) {
+        const int slot = r < rows ? s_slot[r] : -1;
+        if (slot < 0)
+            return;
+        const int64_t row = row0 + r;
+#pragma unroll
+        for (int s = 0; s < LPC; ++s)
+            if (holds[s]) {
+                const float* state = state_at(slot, s);
+                if (VEC) {
+                    const float4 v = *reinterpret_cast<const float4*>(state);
+                    x.h[s][0] = v.x, x.h[s][1] = v.y, x.h[s][2] = v.z, x.h[s][3] = v.w;
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NS; ++n)
+                        if (n < nn)
+                            x.h[s][n] = state[n];
+                }
+            }
+        if (n0 < p.N) {
+            const io_t* B = static_cast<const io_t*>(p.B) + row * p.N + n0;
+            const io_t* C = static_cast<const io_t*>(p.C) + row * p.N + n0;
+            if (VEC) {
+                using raw = typename Pair<io_t>::raw;
+#pragma unroll
+                for (int n = 0; n < 4; n += 2) {
+                    *reinterpret_cast<raw*>(&x.B[n]) = *reinterpret_cast<const raw*>(B + n);
+                    *reinterpret_cast<raw*>(&x.C[n]) = *reinterpret_cast<const raw*>(C + n);
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < NS; ++n)
+                    if (n < nn) {
+                        x.B[n] = B[n];
+                        x.C[n] = C[n];
+                    }
+            }
+        }
+        if (active) {
+            x.u = static_cast<const io_t*>(p.u)[row * p.D + d];
+            x.delta = static_cast<const io_t*>(p.delta)[row * p.D + d];
+            if (p.z)
+                x.z = static_cast<const io_t*>(p.z)[row * p.D + d];
+            const io_t* win = window_at(slot);
 #pragma unroll
             for (int j = 0; j < SS_MAX_CONV_WIDTH - 1; ++j)
                 if (j < width - 1)
-                    c = fmaf(cw[j], ld1(&seen[j]), c);
-            c = fmaf(cw[width - 1], u, c);
-            if (threadIdx.x % LPC == 0) {
+                    x.seen[j] = win[j * p.D];
+        }
+    };
+    auto step = [&](int r, Row<io_t, LPC, NS>& x) {
+        const int slot = s_slot[r];
+        if (slot < 0)
+            return;  // the same for the whole CTA
+        float u = 0.f, delta = 0.f;
+        if (active) {
+            u = ld1(&x.u);
+            if (p.conv_w) {
+                float c = cb;
 #pragma unroll
-                for (int j = 1; j < SS_MAX_CONV_WIDTH - 1; ++j)
+                for (int j = 0; j < SS_MAX_CONV_WIDTH - 1; ++j)
                     if (j < width - 1)
-                        win[(j - 1) * p.D] = seen[j];
-                if (width > 1)
-                    win[(width - 2) * p.D] = *gu;
+                        c = fmaf(cw[j], ld1(&x.seen[j]), c);
+                // (constant indices keep the taps in registers)
+                c = fmaf(width == 4 ? cw[3] : width == 3 ? cw[2] : width == 2 ? cw[1] : cw[0], u, c);
+                if (width > 1) {
+                    io_t* win = window_at(slot);
+#pragma unroll
+                    for (int j = 1; j < SS_MAX_CONV_WIDTH - 1; ++j)
+                        if (j < width - 1)
+                            win[(j - 1) * p.D] = x.seen[j];
+                    win[(width - 2) * p.D] = x.u;
+                }
+                u = silu_f(c);
             }
-            u = silu_f(c);
+            delta = ld1(&x.delta) + bias;
+            if (p.softplus)
+                delta = softplus_f(delta);
         }
-        delta = ld1(static_cast<const io_t*>(p.delta) + row * p.D + d);
-        if (p.bias)
-            delta += p.bias[d];
-        if (p.softplus)
-            delta = softplus_f(delta);
-    }
-    const float w = delta * u, dl = delta * kLog2e;
-    const io_t* gB = static_cast<const io_t*>(p.B) + row * p.N + n0;
-    const io_t* gC = static_cast<const io_t*>(p.C) + row * p.N + n0;
+        const float w = delta * u;
+        float B[NS], C[NS], y = 0.f;
 #pragma unroll
-    for (int n = 0; n < NS; ++n)
-        if (holds && n < nn) {
-            h[n] = fmaf(ex2(dl * A[n]), h[n], w * ld1(gB + n));
-            y = fmaf(h[n], ld1(gC + n), y);
+        for (int n = 0; n < NS; ++n) {
+            const bool used = n0 < p.N && n < nn;
+            B[n] = used ? ld1(&x.B[n]) : 0.f;
+            C[n] = used ? ld1(&x.C[n]) : 0.f;
         }
-    if (VEC) {
-        if (holds)
-            *reinterpret_cast<float4*>(state) = make_float4(h[0], h[1], h[2], h[3]);
-    } else {
 #pragma unroll
-        for (int n = 0; n < NS; ++n)
-            if (holds && n < nn)
-                state[n] = h[n];
-    }
+        for (int s = 0; s < LPC; ++s) {
+            // channel s * CP + lane / LPC of the warp, from the lane that has it
+            const int from = s * CP + lane / LPC;
+            const float dl = LPC > 1 ? __shfl_sync(0xffffffffu, delta, from) : delta;
+            const float ws = LPC > 1 ? __shfl_sync(0xffffffffu, w, from) : w;
+            float part = 0.f;
+            if (holds[s]) {
 #pragma unroll
-    for (int m = LPC / 2; m > 0; m /= 2)
-        y += __shfl_xor_sync(0xffffffffu, y, m);
-    if (active && threadIdx.x % LPC == 0) {
-        if (p.Dskip)
-            y = fmaf(p.Dskip[d], u, y);
-        if (p.z)
-            y *= silu_f(ld1(static_cast<const io_t*>(p.z) + row * p.D + d));
-        st1(static_cast<io_t*>(p.out) + row * p.D + d, y);
+                for (int n = 0; n < NS; ++n)
+                    if (n < nn) {
+                        x.h[s][n] = fmaf(ex2(dl * A[s][n]), x.h[s][n], ws * B[n]);
+                        part = fmaf(x.h[s][n], C[n], part);
+                    }
+                float* state = state_at(slot, s);
+                if (VEC) {
+                    *reinterpret_cast<float4*>(state) =
+                        make_float4(x.h[s][0], x.h[s][1], x.h[s][2], x.h[s][3]);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NS; ++n)
+                        if (n < nn)
+                            state[n] = x.h[s][n];
+                }
+            }
+#pragma unroll
+            for (int m = LPC / 2; m > 0; m /= 2)
+                part += __shfl_xor_sync(0xffffffffu, part, m);
+            // back to the lane of the channel: lane l belongs to pass l / CP
+            const float mine = LPC > 1 ? __shfl_sync(0xffffffffu, part, (lane % CP) * LPC) : part;
+            y = lane / CP == s ? mine : y;
+        }
+        if (active) {
+            y = fmaf(skip, u, y);
+            if (p.z)
+                y *= silu_f(ld1(&x.z));
+            st1(static_cast<io_t*>(p.out) + (row0 + r) * p.D + d, y);
+        }
+    };
+    // slots of different rows are distinct, so a row's loads may pass the stores of the one before
+    Row<io_t, LPC, NS> x[2];
+    load(0, x[0]);
+    for (int r = 0; r < rows; r += 2) {
+        load(r + 1, x[1]);
+        step(r, x[0]);
+        if (r + 1 < rows) {
+            load(r + 2, x[0]);
+            step(r + 1, x[1]);
+        }
     }
 }
 
-template <typename io_t, int LPC, bool VEC> cudaError_t launch(const StepParams& p, cudaStream_t st)
+template <typename io_t, int LPC, bool VEC> cudaError_t launch(StepParams p, cudaStream_t st)
 {
-    constexpr int CH = kThreads / LPC;
-    const int64_t blocks = (p.D + CH - 1) / CH * p.batch;
+    const int64_t tiles = (p.D + kThreads - 1) / kThreads;
+    // as many rows a CTA as still leave four CTAs for each of 148 SMs
+    const int64_t rows = tiles * p.batch / (4 * 148);
+    p.rows = static_cast<int>(rows < 1 ? 1 : rows > kRows ? kRows : rows);
+    const int64_t blocks = tiles * ((p.batch + p.rows - 1) / p.rows);
     step_kernel<io_t, LPC, VEC><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p);
     return cudaGetLastError();
 }
