@@ -151,23 +151,24 @@ struct BwdPlan {
     size_t off_ckpt, off_cum, off_h, off_p, off_g, off_dbc, off_dpar, off_du, off_dz, bytes;
 };
 
-// Automatic segments of the gradient. `units` (direction, batch row, channel tile) CTAs for each
-// segment fill the kBwdSlots CTAs that fit on a B200 (3 on each of 148 SMs) in whole waves: S
-// segments take ceil(units S / slots) / S of a whole sequence's time, any split costs about 15%
-// more work (the segment products, the checkpoints' shift) and each segment 1% (its ends).  Measured, 8 x 2048 x 1536 (192 units):
-// 1434 us unsplit, 923 at S = 2, 887 at 4, 820 at 6, 800 at 9; 64 x 197 x 768 in two directions (1536
-// units): 623 us unsplit, more with any split.  No segment is shorter than 64 steps.
+// Automatic segments of the gradient.  `units` (direction, batch row, channel tile) CTAs for each
+// segment fill the kBwdSlots CTAs that fit on a B200 (3 on each of 148 SMs) in whole waves, so S
+// segments take ceil(units S / slots) / S of a whole sequence's time; a step takes about 0.3 us, any
+// split costs about 15% more work (the segment products, the checkpoints' shift), and every wave
+// folds the other segments' states (0.2 us for each) and has its ends (2.4 us).  Measured: 8 x 2048 x 1536 (192 units) 1434 us unsplit, 923
+// at S = 2, 752 at 9, 758 at 16, 795 at 23, 828 at 30; 2 x 333 x 72 in fp32 (4 units) 232 us unsplit, 108 at 4, 70 at 20, 68 at 40;
+// 64 x 197 x 768 in two directions (1536 units) 601 us unsplit, more with any split.
 constexpr int64_t kBwdSlots = 3 * 148;
-constexpr int64_t kBwdMinSteps = 64;
-constexpr int64_t kBwdMostAuto = 32;
+constexpr int64_t kBwdMinSteps = 16;
+constexpr int64_t kBwdMostAuto = 256;
 
 int64_t bwd_segments(int64_t units, int64_t L)
 {
     int64_t best = 1;
-    double least = static_cast<double>(ceil_div(units, kBwdSlots));
+    double least = 0.3 * static_cast<double>(L * ceil_div(units, kBwdSlots));
     for (int64_t S = 2; S <= kBwdMostAuto && S <= L / kBwdMinSteps; ++S) {
-        const double cost =
-            (1.15 + 0.01 * S) * static_cast<double>(ceil_div(units * S, kBwdSlots)) / S;
+        const double waves = static_cast<double>(ceil_div(units * S, kBwdSlots));
+        const double cost = waves * (0.345 * static_cast<double>(L) / S + 0.2 * S + 2.4);
         if (cost < 0.999 * least) {
             least = cost;
             best = S;
@@ -226,8 +227,9 @@ ss_status plan_bwd(const ss_shape* s, const ss_direction_map* dmap, const ss_lau
     pl->seg_len = ntiles > 0 ? ceil_div(ntiles, want) * so::kBwdTile : so::kBwdTile;
     pl->S = L > 0 ? static_cast<int>(ceil_div(L, pl->seg_len)) : 1;
     pl->split = pl->S > 1 || pl->init != nullptr;
-    if (units * pl->S > kMaxI32 || ceil_div(rows * L * 32, 256) > kMaxI32 ||
-        ceil_div(s->batch * L * s->dim, 1024) > kMaxI32)
+    // the blocks of the sweeps and of the launch that adds up what they leave
+    if (units * pl->S > kMaxI32 ||
+        rows * L / 8 + pl->K * s->dim + 2 * (s->batch * L * s->dim / 1024) + 8 > kMaxI32)
         return SS_ERR_SHAPE;
 
     size_t off = 0;

@@ -31,6 +31,7 @@
 #include <type_traits>
 
 #include "so_device.cuh"
+#include "ss_device.cuh"
 
 namespace so {
 
@@ -460,6 +461,7 @@ __global__ void __launch_bounds__(kBwdThreads) summary_kernel(const __grid_const
         put4(seg_at(p.seg_p, p, un, un.seg), kBwdThreads, P);
         put4(seg_at(p.seg_g, p, un, un.seg), kBwdThreads, G);
     }
+    ss::pdl_launch_dependents();  // the gradient sweep may take this CTA's place
 }
 
 // ------------------------------------------------------------------------- gradient sweep
@@ -571,6 +573,11 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
     load_A<PRECISE>(p, un, x, A);
     float2 dskip = dup(0.f), dbias = dup(0.f);
 
+    const int tiles = (un.t1 - un.t0 + kTL - 1) / kTL;
+    io_t bc[kBC][2];
+    issue<io_t>(p, un, sm.cta, un.t0 + (tiles - 1) * kTL, sm.st[(tiles - 1) & 1], true, bc);
+    ss::pdl_wait();  // from here on the summary sweep's results are read
+
     // the state that enters the segment and the gradient that enters it from behind
     const bool shift = SPLIT && (un.seg > 0 || p.init != nullptr);
     const int64_t cell = (un.kb * p.D + un.c0 + x.c) * p.N;  // of [K, batch, D, N] arrays
@@ -590,6 +597,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
             if (p.init && x.valid && n < p.N)
                 hstart[i] = make_float2(p.init[cell + n], p.init[cell + p.N + n]);
         }
+#pragma unroll 4
         for (int s = 0; s < un.seg; ++s) {
             get4(seg_at(p.seg_p, p, un, s), kBwdThreads, P);
             get4(seg_at(p.seg_h, p, un, s), kBwdThreads, v);
@@ -598,6 +606,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
                 hstart[i] = __ffma2_rn(P[i], hstart[i], v[i]);
         }
         put4(&sm.hstart[0][threadIdx.x], kBwdThreads, hstart);
+#pragma unroll 4
         for (int s = p.S - 1; s > un.seg; --s) {
             get4(seg_at(p.seg_p, p, un, s), kBwdThreads, P);
             get4(seg_at(p.seg_g, p, un, s), kBwdThreads, v);
@@ -607,15 +616,12 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
         }
     }
 
-    const int tiles = (un.t1 - un.t0 + kTL - 1) / kTL;
     int slice = (un.t1 - 1) / kT;  // of the sequence; segments start on slice borders
     // the next slice's checkpoint is on its way while this one is worked on
     float2 next[4], next_cum = dup(0.f);
     get4(ckpt_at(un, sm.cta, slice), kBwdThreads, next);
     if (shift && x.valid)
         next_cum = *cum_at(un, sm.cta, x, slice);
-    io_t bc[kBC][2];
-    issue<io_t>(p, un, sm.cta, un.t0 + (tiles - 1) * kTL, sm.st[(tiles - 1) & 1], true, bc);
     for (int it = tiles - 1; it >= 0; --it) {
         const int t = un.t0 + it * kTL;
         const Stage<io_t>& st = sm.st[it & 1];
@@ -729,71 +735,23 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
         par_out[kNP + 2 + kNP] = dskip.y;
         par_out[kNP + 2 + kNP + 1] = dbias.y;
     }
+    ss::pdl_launch_dependents();
 }
 
 // ------------------------------------------------------------------------- the last sums
 
-// dB, dC = sum over the channel tiles; a thread has one element.
-template <typename io_t>
-__global__ void __launch_bounds__(256) sum_dbc_kernel(const __grid_constant__ BwdParams p)
-{
-    const int64_t i = blockIdx.x * int64_t{256} + threadIdx.x;
-    const int64_t ctiles = (p.D + kC - 1) / kC;
-    if (i >= p.K * p.batch * p.L * 2 * kNP)
-        return;
-    const int64_t row = i / (2 * kNP);  // kb * L + t
-    const int j = static_cast<int>(i % (2 * kNP));
-    const int64_t kb = row / p.L, t = row - kb * p.L;
-    const float* src = p.dbc + (kb * ctiles * p.L + t) * 2 * kNP + j;
-    float v = 0.f;
-    for (int64_t c = 0; c < ctiles; ++c)
-        v += src[c * p.L * 2 * kNP];
-    const int n = j % kNP;
-    if (n < p.N)
-        st1(static_cast<io_t*>(j < kNP ? p.g.dB : p.g.dC) + row * p.N + n, v);
-}
+// Blocks [0, bc_blocks): dB, dC = sum over the channel tiles; a thread has one element.
+// The next par_blocks x sets: dA, dDskip, ddelta_bias = sum over (direction,) batch rows and
+// segments; 32 columns by 8 groups of rows a CTA.
+// The rest: du and dz = sum over the directions' parts, four elements a thread.
+struct FinishGrid {
+    unsigned bc_blocks, par_blocks, sets, dir_blocks;
+};
 
-// dA, dDskip, ddelta_bias = sum over (direction,) batch rows and segments: 32 columns by 8 groups
-// of rows a CTA.
-__global__ void __launch_bounds__(256) sum_par_kernel(const __grid_constant__ BwdParams p)
-{
-    __shared__ float s[8][33];
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    const int64_t cols = p.D * (kNP + 2);
-    const int64_t col = blockIdx.x * int64_t{32} + x;
-    const int64_t sets = p.params_per_dir ? p.K : 1;
-    const int64_t rows = p.K * p.batch * p.S / sets;
-    const int64_t set = blockIdx.y;
-    const int64_t d = col / (kNP + 2);
-    const int j = static_cast<int>(col - d * (kNP + 2));
-    const bool used = col < cols && (j < p.N || j >= kNP);
-    float v = 0.f;
-    if (used)
-        for (int64_t r = y; r < rows; r += 8)
-            v += p.dpar[(set * rows + r) * cols + col];
-    s[y][x] = v;
-    __syncthreads();
-    if (y == 0 && used) {
-#pragma unroll
-        for (int i = 1; i < 8; ++i)
-            v += s[i][x];
-        if (j < p.N)
-            p.g.dA[(set * p.D + d) * p.N + j] = v;
-        else if (j == kNP && p.g.dDskip)
-            p.g.dDskip[set * p.D + d] = v;
-        else if (j == kNP + 1 && p.g.ddelta_bias)
-            p.g.ddelta_bias[set * p.D + d] = v;
-    }
-}
-
-// du or dz = sum over the directions' parts, four elements a thread.
 template <typename io_t>
-__global__ void __launch_bounds__(256) sum_dirs_kernel(const float* part, io_t* out, int64_t n, int K)
+__device__ __forceinline__ void sum_dirs(const float* part, io_t* out, int64_t i, int64_t n, int K)
 {
     using P2 = Pair<io_t>;
-    const int64_t i = 4 * (blockIdx.x * int64_t{256} + threadIdx.x);
-    if (i >= n)
-        return;
     float4 v = *reinterpret_cast<const float4*>(part + i);
     for (int k = 1; k < K; ++k) {
         const float4 w = *reinterpret_cast<const float4*>(part + k * n + i);
@@ -805,6 +763,72 @@ __global__ void __launch_bounds__(256) sum_dirs_kernel(const float* part, io_t* 
     typename P2::raw* o = reinterpret_cast<typename P2::raw*>(out + i);
     o[0] = P2::r(make_float2(v.x, v.y));
     o[1] = P2::r(make_float2(v.z, v.w));
+}
+
+template <typename io_t>
+__global__ void __launch_bounds__(256)
+    finish_kernel(const __grid_constant__ BwdParams p, const __grid_constant__ FinishGrid grid)
+{
+    __shared__ float s[8][33];
+    ss::pdl_wait();
+    unsigned block = blockIdx.x;
+    if (block < grid.bc_blocks) {
+        const int64_t i = block * int64_t{256} + threadIdx.x;
+        const int64_t ctiles = (p.D + kC - 1) / kC;
+        if (i >= p.K * p.batch * p.L * 2 * kNP)
+            return;
+        const int64_t row = i / (2 * kNP);  // kb * L + t
+        const int j = static_cast<int>(i % (2 * kNP));
+        const int64_t kb = row / p.L, t = row - kb * p.L;
+        const float* src = p.dbc + (kb * ctiles * p.L + t) * 2 * kNP + j;
+        float v = 0.f;
+#pragma unroll 4
+        for (int64_t c = 0; c < ctiles; ++c)
+            v += src[c * p.L * 2 * kNP];
+        const int n = j % kNP;
+        if (n < p.N)
+            st1(static_cast<io_t*>(j < kNP ? p.g.dB : p.g.dC) + row * p.N + n, v);
+        return;
+    }
+    block -= grid.bc_blocks;
+    if (block < grid.par_blocks * grid.sets) {
+        const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+        const int64_t cols = p.D * (kNP + 2);
+        const int64_t set = block / grid.par_blocks;
+        const int64_t col = (block - set * grid.par_blocks) * int64_t{32} + x;
+        const int64_t rows = p.K * p.batch * p.S / grid.sets;
+        const int64_t d = col / (kNP + 2);
+        const int j = static_cast<int>(col - d * (kNP + 2));
+        const bool used = col < cols && (j < p.N || j >= kNP);
+        float v = 0.f;
+        if (used)
+#pragma unroll 4
+            for (int64_t r = y; r < rows; r += 8)
+                v += p.dpar[(set * rows + r) * cols + col];
+        s[y][x] = v;
+        __syncthreads();
+        if (y == 0 && used) {
+#pragma unroll
+            for (int i = 1; i < 8; ++i)
+                v += s[i][x];
+            if (j < p.N)
+                p.g.dA[(set * p.D + d) * p.N + j] = v;
+            else if (j == kNP && p.g.dDskip)
+                p.g.dDskip[set * p.D + d] = v;
+            else if (j == kNP + 1 && p.g.ddelta_bias)
+                p.g.ddelta_bias[set * p.D + d] = v;
+        }
+        return;
+    }
+    block -= grid.par_blocks * grid.sets;
+    const int64_t n = p.batch * p.L * p.D;  // a multiple of 4
+    const int64_t i = 4 * ((block % grid.dir_blocks) * int64_t{256} + threadIdx.x);
+    if (i >= n)
+        return;
+    if (block < grid.dir_blocks && p.du_part)
+        sum_dirs(p.du_part, static_cast<io_t*>(p.g.du), i, n, p.K);
+    else
+        sum_dirs(p.dz_part, static_cast<io_t*>(p.g.dz), i, n, p.K);
 }
 
 template <typename io_t, bool SPLIT> cudaError_t launch_sweeps(const BwdParams& p, cudaStream_t st)
@@ -820,27 +844,37 @@ template <typename io_t, bool SPLIT> cudaError_t launch_sweeps(const BwdParams& 
     const unsigned blocks =
         static_cast<unsigned>((p.D + kC - 1) / kC * p.batch * p.K * p.S);
     summary_kernel<io_t, SPLIT><<<blocks, kBwdThreads, sizeof(SumSmem<io_t>), st>>>(p);
-    grad_kernel<io_t, SPLIT><<<blocks, kBwdThreads, sizeof(GradSmem<io_t>), st>>>(p);
-    return cudaGetLastError();
+    e = cudaGetLastError();
+    if (e == cudaSuccess)
+        e = ss::launch_ex(grad_kernel<io_t, SPLIT>, blocks, kBwdThreads, sizeof(GradSmem<io_t>), st,
+                          true, p);
+    return e;
 }
 
 template <typename io_t> cudaError_t launch_bwd_io(const BwdParams& p, cudaStream_t st)
 {
-    cudaError_t e = p.S > 1 || p.init ? launch_sweeps<io_t, true>(p, st)
-                                      : launch_sweeps<io_t, false>(p, st);
+    const cudaError_t e = p.S > 1 || p.init ? launch_sweeps<io_t, true>(p, st)
+                                            : launch_sweeps<io_t, false>(p, st);
     if (e != cudaSuccess)
         return e;
-    const int64_t nbc = p.K * p.batch * p.L * 2 * kNP;
-    sum_dbc_kernel<io_t><<<static_cast<unsigned>((nbc + 255) / 256), 256, 0, st>>>(p);
-    const dim3 grid(static_cast<unsigned>((p.D * (kNP + 2) + 31) / 32), p.params_per_dir ? p.K : 1);
-    sum_par_kernel<<<grid, 256, 0, st>>>(p);
-    const int64_t n = p.batch * p.L * p.D;
-    const unsigned nb = static_cast<unsigned>((n / 4 + 255) / 256);
-    if (p.du_part)
-        sum_dirs_kernel<io_t><<<nb, 256, 0, st>>>(p.du_part, static_cast<io_t*>(p.g.du), n, p.K);
-    if (p.dz_part)
-        sum_dirs_kernel<io_t><<<nb, 256, 0, st>>>(p.dz_part, static_cast<io_t*>(p.g.dz), n, p.K);
-    return cudaGetLastError();
+    const int64_t nbc = p.K * p.batch * p.L * 2 * kNP, n = p.batch * p.L * p.D;
+    FinishGrid g;
+    g.bc_blocks = static_cast<unsigned>((nbc + 255) / 256);
+    g.par_blocks = static_cast<unsigned>((p.D * (kNP + 2) + 31) / 32);
+    g.sets = p.params_per_dir ? p.K : 1;
+    g.dir_blocks = static_cast<unsigned>((n / 4 + 255) / 256);
+    const unsigned merges = (p.du_part ? 1 : 0) + (p.dz_part ? 1 : 0);
+    const unsigned blocks = g.bc_blocks + g.par_blocks * g.sets + g.dir_blocks * merges;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, finish_kernel<io_t>, p, g);
 }
 
 }  // namespace

@@ -11,6 +11,7 @@ wrap forward and gradient for torch.autograd.  There is no CPU path.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -68,17 +69,19 @@ def load():
     return _lib
 
 
-def _check(t, name, shape, dtype, device):
-    """Optional tensors may be None; the rest is what the C call relies on."""
-    if t is None:
-        return
-    if t.device != device:
-        raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.dtype is not dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if not t.is_contiguous():
+def _check(device, *tensors):
+    """Each (name, tensor, shape, dtype) is what the C call relies on; a tensor may be None."""
+    index = device.index
+    for name, t, shape, dtype in tensors:
+        if t is None or (t.shape == shape and t.dtype is dtype and t.get_device() == index and
+                         t.is_contiguous()):
+            continue
+        if t.device != device:
+            raise ValueError("%s must be a CUDA tensor on %s" % (name, device))
+        if t.shape != shape:
+            raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+        if t.dtype is not dtype:
+            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
         raise ValueError("%s must be contiguous" % name)
 
 
@@ -97,7 +100,8 @@ def _ptr(t):
 
 
 def _stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+    # (the stream object of torch.cuda.current_stream costs 2 us, half of a small call)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _done(status, what):
@@ -117,13 +121,11 @@ def _recurrence_args(x, gate, gate_bias, initial_state, form, complement, revers
     io = _io_code(x.dtype)
     device = _device_of(x, "x")
     b, L, D = x.shape
-    _check(x, "x", (b, L, D), x.dtype, device)
-    _check(gate, "gate", (b, L, D), x.dtype, device)
-    _check(gate_bias, "gate_bias", (D,), _F32, device)
-    _check(initial_state, "initial_state", (b, D), _F32, device)
-    opts = SsRecurrenceOpts(GATE_FORMS[form], int(bool(complement)),
+    _check(device, ("x", x, (b, L, D), x.dtype), ("gate", gate, (b, L, D), x.dtype),
+           ("gate_bias", gate_bias, (D,), _F32), ("initial_state", initial_state, (b, D), _F32))
+    opts = SsRecurrenceOpts(GATE_FORMS[form], 1 if complement else 0,
                             SS_DIR_REV if reverse else SS_DIR_FWD, 0)
-    return device, make_shape(b, L, D, 1, io), opts, (b, L, D)
+    return device, SsShape(b, L, D, 1, io, 0), opts, (b, L, D)
 
 
 def gated_recurrence_workspace_size(shape: SsShape, opts: SsRecurrenceOpts, backward: bool) -> int:
@@ -132,6 +134,13 @@ def gated_recurrence_workspace_size(shape: SsShape, opts: SsRecurrenceOpts, back
                                                  int(bool(backward)), ctypes.byref(n)),
           "gated_recurrence_workspace_size")
     return n.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _recurrence_workspace(b, L, D, io, form, backward):
+    """The size goes by the sizes alone: asked once for each."""
+    return gated_recurrence_workspace_size(SsShape(b, L, D, 1, io, 0),
+                                           SsRecurrenceOpts(form, 0, SS_DIR_FWD, 0), backward)
 
 
 def _workspace(nbytes, device):
@@ -156,11 +165,12 @@ def gated_recurrence_fwd(x, gate, gate_bias=None, initial_state=None, form="sigm
     if out is None:
         out = torch.empty_like(x)
     else:
-        _check(out, "out", (b, L, D), x.dtype, device)
-    if return_last_state and last_state is None:
+        _check(device, ("out", out, (b, L, D), x.dtype))
+    if last_state is not None:
+        _check(device, ("last_state", last_state, (b, D), _F32))
+    elif return_last_state:
         last_state = torch.empty((b, D), dtype=_F32, device=device)
-    _check(last_state, "last_state", (b, D), _F32, device)
-    n = gated_recurrence_workspace_size(shape, opts, False)
+    n = _recurrence_workspace(b, L, D, shape.io_dtype, opts.form, False)
     ws = _workspace(n, device)
     _done(load().gated_recurrence_fwd(ctypes.byref(shape), ctypes.byref(opts), x.data_ptr(),
                                       gate.data_ptr(), _ptr(gate_bias), _ptr(initial_state),
@@ -176,13 +186,12 @@ def gated_recurrence_bwd(dout, x, gate, out, gate_bias=None, initial_state=None,
     dtype; dlast_state [batch, D] float32 or None, the gradient of the last state."""
     device, shape, opts, (b, L, D) = _recurrence_args(x, gate, gate_bias, initial_state, form,
                                                       complement, reverse)
-    _check(out, "out", (b, L, D), x.dtype, device)
-    _check(dout, "dout", (b, L, D), x.dtype, device)
-    _check(dlast_state, "dlast_state", (b, D), _F32, device)
+    _check(device, ("out", out, (b, L, D), x.dtype), ("dout", dout, (b, L, D), x.dtype),
+           ("dlast_state", dlast_state, (b, D), _F32))
     dx, dgate = torch.empty_like(x), torch.empty_like(x)
     dbias = None if gate_bias is None else torch.empty_like(gate_bias)
     dinit = None if initial_state is None else torch.empty_like(initial_state)
-    n = gated_recurrence_workspace_size(shape, opts, True)
+    n = _recurrence_workspace(b, L, D, shape.io_dtype, opts.form, True)
     ws = _workspace(n, device)
     _done(load().gated_recurrence_bwd(ctypes.byref(shape), ctypes.byref(opts), x.data_ptr(),
                                       gate.data_ptr(), _ptr(gate_bias), _ptr(initial_state),
@@ -202,6 +211,14 @@ def selective_scan_bwd_workspace_size(shape: SsShape, dmap: SsDirectionMap | Non
         ctypes.byref(opts) if opts is not None else None, ctypes.byref(n)),
         "selective_scan_bwd_workspace_size")
     return n.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _bwd_workspace(batch, L, D, N, io, dirs, H, W, segments, flags, initial):
+    """The size goes by the sizes and options alone (of the initial state only whether there is
+    one): asked once for each."""
+    return selective_scan_bwd_workspace_size(make_shape(batch, L, D, N, io), make_dirmap(dirs, H, W),
+                                             make_opts(segments, flags, None, 16 if initial else 0))
 
 
 def selective_scan_bwd(dout, u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=True,
@@ -236,17 +253,13 @@ def selective_scan_bwd(dout, u, delta, A, B, C, D=None, z=None, delta_bias=None,
         pshape = (K, Dm)
     io = u.dtype
     code = _io_code(io)
-    _check(u, "u", tuple(u.shape[:-3]) + (batch, L, Dm), io, device)
-    _check(delta, "delta", lead + (batch, L, Dm), io, device)
-    _check(B, "B", leadB + (batch, L, N), io, device)
-    _check(C, "C", leadC + (batch, L, N), io, device)
-    _check(z, "z", (batch, L, Dm), io, device)
-    _check(dout, "dout", (batch, L, Dm), io, device)
-    _check(A, "A", pshape + (N,), _F32, device)
-    _check(D, "D", pshape, _F32, device)
-    _check(delta_bias, "delta_bias", pshape, _F32, device)
-    _check(initial_state, "initial_state", (K, batch, Dm, N), _F32, device)
-    _check(dlast_state, "dlast_state", (K, batch, Dm, N), _F32, device)
+    rows = (batch, L, Dm)
+    _check(device, ("u", u, u.shape, io), ("delta", delta, lead + rows, io),
+           ("B", B, leadB + (batch, L, N), io), ("C", C, leadC + (batch, L, N), io),
+           ("z", z, rows, io), ("dout", dout, rows, io), ("A", A, pshape + (N,), _F32),
+           ("D", D, pshape, _F32), ("delta_bias", delta_bias, pshape, _F32),
+           ("initial_state", initial_state, (K, batch, Dm, N), _F32),
+           ("dlast_state", dlast_state, (K, batch, Dm, N), _F32))
 
     def like(t):
         return None if t is None else torch.empty_like(t)
@@ -257,7 +270,8 @@ def selective_scan_bwd(dout, u, delta, A, B, C, D=None, z=None, delta_bias=None,
     shape = make_shape(batch, L, Dm, N, code)
     dmap = make_dirmap(dirs, H, W)
     opts = make_opts(segments, flags, None, _ptr(initial_state) or 0)
-    n = selective_scan_bwd_workspace_size(shape, dmap, opts)
+    n = _bwd_workspace(batch, L, Dm, N, code, tuple(dirs), H, W, segments, flags,
+                       initial_state is not None)
     ws = _workspace(n, device)
     _done(load().selective_scan_bwd(
         ctypes.byref(shape), u.data_ptr(), delta.data_ptr(), A.data_ptr(), B.data_ptr(),
@@ -291,32 +305,25 @@ def selective_scan_step(u, delta, A, B, C, state, D=None, z=None, delta_bias=Non
     if state.dim() != 3:
         raise ValueError("state must be [num_slots, D, N]")
     num_slots = state.shape[0]
-    _check(u, "u", (batch, Dm), io, device)
-    _check(delta, "delta", (batch, Dm), io, device)
-    _check(B, "B", (batch, N), io, device)
-    _check(C, "C", (batch, N), io, device)
-    _check(z, "z", (batch, Dm), io, device)
-    _check(A, "A", (Dm, N), _F32, device)
-    _check(D, "D", (Dm,), _F32, device)
-    _check(delta_bias, "delta_bias", (Dm,), _F32, device)
-    _check(state, "state", (num_slots, Dm, N), _F32, device)
-    _check(slots, "slots", (batch,), _I32, device)
+    row, group, channel = (batch, Dm), (batch, N), (Dm,)
+    _check(device, ("u", u, row, io), ("delta", delta, row, io), ("B", B, group, io),
+           ("C", C, group, io), ("z", z, row, io), ("A", A, (Dm, N), _F32), ("D", D, channel, _F32),
+           ("delta_bias", delta_bias, channel, _F32), ("state", state, (num_slots, Dm, N), _F32),
+           ("slots", slots, (batch,), _I32), ("out", out, row, io))
     width = 0
     if conv_weight is not None:
         width = conv_weight.shape[-1]
         if not 1 <= width <= SS_MAX_CONV_WIDTH:
             raise ValueError("conv_weight must be [D, width] with 1 to %d taps" % SS_MAX_CONV_WIDTH)
-        _check(conv_weight, "conv_weight", (Dm, width), _F32, device)
-        _check(conv_bias, "conv_bias", (Dm,), _F32, device)
         if conv_state is None and width > 1:
             raise ValueError("conv_weight needs conv_state")
-        _check(conv_state, "conv_state", (num_slots, width - 1, Dm), io, device)
+        _check(device, ("conv_weight", conv_weight, (Dm, width), _F32),
+               ("conv_bias", conv_bias, channel, _F32),
+               ("conv_state", conv_state, (num_slots, width - 1, Dm), io))
     elif conv_bias is not None or conv_state is not None:
         raise ValueError("conv_bias and conv_state need conv_weight")
     if out is None:
         out = torch.zeros_like(u) if slots is not None else torch.empty_like(u)
-    else:
-        _check(out, "out", (batch, Dm), io, device)
     _done(load().selective_scan_step(
         ctypes.byref(SsShape(batch, 1, Dm, N, code, 0)), num_slots, u.data_ptr(), delta.data_ptr(),
         A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D), _ptr(z), _ptr(delta_bias),
@@ -335,9 +342,8 @@ def _state_args(state, codes, scales, bits, src_slots, dst_slots, src_pool, dst_
         raise ValueError("state and codes must be [slots, D, ...]")
     slots, Dm, N = state.shape
     parked = codes.shape[0]
-    _check(state, "state", (slots, Dm, N), _F32, device)
-    _check(codes, "codes", (parked, Dm, N if bits == 8 else (N + 1) // 2), _I8, device)
-    _check(scales, "scales", (parked, Dm), _F32, device)
+    _check(device, ("state", state, (slots, Dm, N), _F32), ("scales", scales, (parked, Dm), _F32),
+           ("codes", codes, (parked, Dm, N if bits == 8 else (N + 1) // 2), _I8))
     rows = None
     for t, name in ((src_slots, "src_slots"), (dst_slots, "dst_slots")):
         if t is not None:
@@ -346,7 +352,7 @@ def _state_args(state, codes, scales, bits, src_slots, dst_slots, src_pool, dst_
             if rows is not None and t.shape[0] != rows:
                 raise ValueError("src_slots and dst_slots must have one length")
             rows = t.shape[0]
-            _check(t, name, (rows,), _I32, device)
+            _check(device, (name, t, (rows,), _I32))
     if rows is None:
         rows = src_pool.shape[0]
     return device, rows, Dm, N, slots, parked
