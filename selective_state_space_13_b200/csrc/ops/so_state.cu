@@ -16,6 +16,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
+// Pieces of 32 channels that a warp does for one look at the row's slots; their loads are all in
+// flight before that look.
+constexpr int kChunks = 2;
+constexpr int kCtaChannels = kThreads * kChunks;
 
 // The codes of NS states, as bytes; amax is finite and not zero.
 template <int NS>
@@ -23,14 +27,18 @@ __device__ __forceinline__ void codes_of(const float* h, float amax, int q, uint
 {
     // inv is 0 or infinite where q / amax leaves the fp32 range: those go the long way
     const float inv = static_cast<float>(q) * rcp(amax);
-    const float magic = 12582912.f;  // 1.5 * 2^23: adding it leaves the rounded integer in the low bits
+    // adding 1.5 * 2^23 leaves the rounded integer in the low bits
+    const float2 magic = make_float2(12582912.f, 12582912.f);
     float off = inv > 0.f && inv < 1e30f ? 0.f : 1.f;
 #pragma unroll
-    for (int n = 0; n < NS; ++n) {
-        const float v = h[n] * inv;
-        const float t = v + magic;
-        off = fmaxf(off, fabsf(v - (t - magic)));  // 1/2 on a border
-        code[n] = __float_as_uint(t);
+    for (int n = 0; n < NS; n += 2) {
+        const float2 v = __fmul2_rn(make_float2(h[n], h[n + 1]), make_float2(inv, inv));
+        const float2 t = __fadd2_rn(v, magic);
+        const float2 r = __fadd2_rn(t, make_float2(-magic.x, -magic.y));
+        const float2 e = __fadd2_rn(v, make_float2(-r.x, -r.y));  // 1/2 on a border
+        off = fmaxf(off, fmaxf(fabsf(e.x), fabsf(e.y)));
+        code[n] = __float_as_uint(t.x);
+        code[n + 1] = __float_as_uint(t.y);
     }
     if (off > 0.5f - 1e-4f) {
 #pragma unroll
@@ -48,9 +56,15 @@ template <> struct Unit<8> {
     {
         return __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
     }
-    static __device__ __forceinline__ int get(type v, int n)
+    // the four codes as floats: a byte, its sign bit flipped, in the low bits of 2^23
+    static __device__ __forceinline__ float4 get(type v)
     {
-        return static_cast<int8_t>(v >> (8 * n));
+        v ^= 0x80808080u;
+        auto f = [&](int n) { return __uint_as_float(__byte_perm(v, 0x4b000000u, 0x7540 + n)); };
+        const float2 back = make_float2(-8388736.f, -8388736.f);  // -(2^23 + 128)
+        const float2 a = __fadd2_rn(make_float2(f(0), f(1)), back);
+        const float2 b = __fadd2_rn(make_float2(f(2), f(3)), back);
+        return make_float4(a.x, a.y, b.x, b.y);
     }
 };
 template <> struct Unit<4> {
@@ -59,9 +73,14 @@ template <> struct Unit<4> {
     {
         return static_cast<type>((c[0] & 15) | (c[1] & 15) << 4 | (c[2] & 15) << 8 | c[3] << 12);
     }
-    static __device__ __forceinline__ int get(type v, int n)
+    static __device__ __forceinline__ float4 get(type v)
     {
-        return static_cast<int>(static_cast<uint32_t>(v) << (28 - 4 * n)) >> 28;
+        const uint32_t w = v ^ 0x8888u;
+        auto f = [&](int n) { return __uint_as_float((w >> (4 * n) & 15u) | 0x4b000000u); };
+        const float2 back = make_float2(-8388616.f, -8388616.f);  // -(2^23 + 8)
+        const float2 a = __fadd2_rn(make_float2(f(0), f(1)), back);
+        const float2 b = __fadd2_rn(make_float2(f(2), f(3)), back);
+        return make_float4(a.x, a.y, b.x, b.y);
     }
 };
 
@@ -72,9 +91,11 @@ struct Place {
 
     __device__ __forceinline__ bool set(const StateParams& p)
     {
-        const int64_t tiles = (p.D + kThreads - 1) / kThreads;
-        row = blockIdx.x / tiles;
-        d0 = (blockIdx.x % tiles) * kThreads + (threadIdx.x >> 5) * 32;
+        // (unsigned: a 64-bit division costs as many instructions as the rest of a short kernel)
+        const unsigned tiles = (static_cast<unsigned>(p.D) + kCtaChannels - 1) / kCtaChannels;
+        const unsigned r = blockIdx.x / tiles;
+        row = r;
+        d0 = (blockIdx.x - r * tiles) * kCtaChannels + (threadIdx.x >> 5) * 32 * kChunks;
         src = p.src ? p.src[row] : row;
         dst = p.dst ? p.dst[row] : row;
         return src >= 0 && src < p.src_slots && dst >= 0 && dst < p.dst_slots;
@@ -95,41 +116,46 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const StateParams p)
     Place at;
     if (!at.set(p))
         return;
-    const int lane = threadIdx.x & 31, ng = lane % LPC;
-    float4 h[LPC];
+    const int lane = threadIdx.x & 31, ng = lane % LPC, units = p.N / 4;
+    float4 h[kChunks][LPC];
 #pragma unroll
-    for (int s = 0; s < LPC; ++s) {
-        const int64_t d = at.d0 + s * CP + lane / LPC;
-        h[s] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (d < p.D && 4 * ng < p.N)
-            h[s] = *reinterpret_cast<const float4*>(p.state_in + (at.src * p.D + d) * p.N + 4 * ng);
-    }
+    for (int j = 0; j < kChunks; ++j)
+#pragma unroll
+        for (int s = 0; s < LPC; ++s) {
+            const int64_t d = at.d0 + 32 * j + s * CP + lane / LPC;
+            h[j][s] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (d < p.D && ng < units)
+                h[j][s] = reinterpret_cast<const float4*>(p.state_in)[(at.src * p.D + d) * units + ng];
+        }
     if (p.dst && slot_taken(p.dst, at.row, static_cast<int32_t>(at.dst), p.src, p.src_slots))
         return;
-    unsigned mine = 0;  // the largest magnitude of channel d0 + lane
 #pragma unroll
-    for (int s = 0; s < LPC; ++s) {
-        const float v[4] = {h[s].x, h[s].y, h[s].z, h[s].w};
-        // by their bits, so that NaN and infinity stand above every number
-        unsigned top = 0;
+    for (int j = 0; j < kChunks; ++j, at.d0 += 32) {
+        unsigned mine = 0;  // the largest magnitude of channel d0 + lane
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-            top = max(top, __float_as_uint(v[n]) & 0x7fffffffu);
+        for (int s = 0; s < LPC; ++s) {
+            const float v[4] = {h[j][s].x, h[j][s].y, h[j][s].z, h[j][s].w};
+            // by their bits, so that NaN and infinity stand above every number
+            unsigned top = 0;
 #pragma unroll
-        for (int m = LPC / 2; m > 0; m /= 2)
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
-        const unsigned back = LPC > 1 ? __shfl_sync(0xffffffffu, top, (lane % CP) * LPC) : top;
-        mine = lane / CP == s ? back : mine;
-        uint32_t code[4] = {0, 0, 0, 0};
-        if (top - 1 < 0x7f7fffffu)  // neither zero nor infinite nor NaN
-            codes_of<4>(v, __uint_as_float(top), Q, code);
-        const int64_t d = at.d0 + s * CP + lane / LPC;
-        if (d < p.D && 4 * ng < p.N)
-            reinterpret_cast<unit_t*>(p.codes)[(at.dst * p.D + d) * (p.N / 4) + ng] =
-                Unit<BITS>::pack(code);
+            for (int n = 0; n < 4; ++n)
+                top = max(top, __float_as_uint(v[n]) & 0x7fffffffu);
+#pragma unroll
+            for (int m = LPC / 2; m > 0; m /= 2)
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, m));
+            const unsigned back = LPC > 1 ? __shfl_sync(0xffffffffu, top, (lane % CP) * LPC) : top;
+            mine = lane / CP == s ? back : mine;
+            uint32_t code[4] = {0, 0, 0, 0};
+            if (top - 1 < 0x7f7fffffu)  // neither zero nor infinite nor NaN
+                codes_of<4>(v, __uint_as_float(top), Q, code);
+            const int64_t d = at.d0 + s * CP + lane / LPC;
+            if (d < p.D && ng < units)
+                reinterpret_cast<unit_t*>(p.codes)[(at.dst * p.D + d) * units + ng] =
+                    Unit<BITS>::pack(code);
+        }
+        if (at.d0 + lane < p.D)
+            p.scales[at.dst * p.D + at.d0 + lane] = scale_of(mine, Q);
     }
-    if (at.d0 + lane < p.D)
-        p.scales[at.dst * p.D + at.d0 + lane] = scale_of(mine, Q);
 }
 
 template <int LPC, int BITS>
@@ -144,36 +170,45 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const StateParams p)
     Place at;
     if (!at.set(p))
         return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ng = lane % LPC;
-    const int64_t d = at.d0 + lane;
-    const int units = p.N / 4;
-    float scale = 0.f;
-    Codes c = {};
-    if (d < p.D) {
-        const unit_t* from = reinterpret_cast<const unit_t*>(p.codes) + (at.src * p.D + d) * units;
-        scale = p.scales[at.src * p.D + d];
-        if (units == LPC) {
-            c = *reinterpret_cast<const Codes*>(from);
-        } else {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ng = lane % LPC, units = p.N / 4;
+    float scale[kChunks];
+    Codes c[kChunks];
 #pragma unroll
-            for (int i = 0; i < LPC; ++i)
-                if (i < units)
-                    c.v[i] = from[i];
+    for (int j = 0; j < kChunks; ++j) {
+        scale[j] = 0.f;
+        c[j] = {};
+        if (at.d0 + 32 * j + lane < p.D) {
+            const int64_t d = at.src * p.D + at.d0 + 32 * j + lane;
+            const unit_t* from = reinterpret_cast<const unit_t*>(p.codes) + d * units;
+            scale[j] = p.scales[d];
+            if (units == LPC) {
+                c[j] = *reinterpret_cast<const Codes*>(from);
+            } else {
+#pragma unroll
+                for (int i = 0; i < LPC; ++i)
+                    if (i < units)
+                        c[j].v[i] = from[i];
+            }
         }
     }
     if (p.dst && slot_taken(p.dst, at.row, static_cast<int32_t>(at.dst), p.src, p.src_slots))
         return;
-    s_codes[warp][lane] = c;
-    __syncwarp();
 #pragma unroll
-    for (int s = 0; s < LPC; ++s) {
-        const int ch = s * CP + lane / LPC;
-        const float sc = __shfl_sync(0xffffffffu, scale, ch);
-        const unit_t v = s_codes[warp][ch].v[ng];
-        if (at.d0 + ch < p.D && 4 * ng < p.N)
-            *reinterpret_cast<float4*>(p.state_out + (at.dst * p.D + at.d0 + ch) * p.N + 4 * ng) =
-                make_float4(Unit<BITS>::get(v, 0) * sc, Unit<BITS>::get(v, 1) * sc,
-                            Unit<BITS>::get(v, 2) * sc, Unit<BITS>::get(v, 3) * sc);
+    for (int j = 0; j < kChunks; ++j, at.d0 += 32) {
+        __syncwarp();  // the codes before these are read
+        s_codes[warp][lane] = c[j];
+        __syncwarp();
+#pragma unroll
+        for (int s = 0; s < LPC; ++s) {
+            const int ch = s * CP + lane / LPC;
+            const float sc = __shfl_sync(0xffffffffu, scale[j], ch);
+            const float4 v = Unit<BITS>::get(s_codes[warp][ch].v[ng]);
+            const float2 a = __fmul2_rn(make_float2(v.x, v.y), make_float2(sc, sc));
+            const float2 b = __fmul2_rn(make_float2(v.z, v.w), make_float2(sc, sc));
+            if (at.d0 + ch < p.D && ng < units)
+                reinterpret_cast<float4*>(p.state_out)[(at.dst * p.D + at.d0 + ch) * units + ng] =
+                    make_float4(a.x, a.y, b.x, b.y);
+        }
     }
 }
 
@@ -185,31 +220,33 @@ __global__ void __launch_bounds__(kThreads) store_any_kernel(const StateParams p
     Place at;
     if (!at.set(p))
         return;
-    const int64_t d = at.d0 + (threadIdx.x & 31);
     if (p.dst && slot_taken(p.dst, at.row, static_cast<int32_t>(at.dst), p.src, p.src_slots))
         return;
-    if (d >= p.D)
-        return;
-    const float* state = p.state_in + (at.src * p.D + d) * p.N;
-    float h[NS];
-    unsigned top = 0;
-    uint32_t code[NS];
+    for (int j = 0; j < kChunks; ++j) {
+        const int64_t d = at.d0 + 32 * j + (threadIdx.x & 31);
+        if (d >= p.D)
+            return;
+        const float* state = p.state_in + (at.src * p.D + d) * p.N;
+        float h[NS];
+        unsigned top = 0;
+        uint32_t code[NS];
 #pragma unroll
-    for (int n = 0; n < NS; ++n) {
-        h[n] = n < p.N ? state[n] : 0.f;
-        top = max(top, __float_as_uint(h[n]) & 0x7fffffffu);
-        code[n] = 0;
+        for (int n = 0; n < NS; ++n) {
+            h[n] = n < p.N ? state[n] : 0.f;
+            top = max(top, __float_as_uint(h[n]) & 0x7fffffffu);
+            code[n] = 0;
+        }
+        if (top - 1 < 0x7f7fffffu)
+            codes_of<NS>(h, __uint_as_float(top), Q, code);
+        p.scales[at.dst * p.D + d] = scale_of(top, Q);
+        const int bytes = BITS == 8 ? p.N : (p.N + 1) / 2;
+        uint8_t* o = p.codes + (at.dst * p.D + d) * bytes;
+#pragma unroll
+        for (int i = 0; i < NS * BITS / 8; ++i)
+            if (i < bytes)
+                o[i] = static_cast<uint8_t>(
+                    BITS == 8 ? code[i] : (code[2 * i % NS] & 15) | code[(2 * i + 1) % NS] << 4);
     }
-    if (top - 1 < 0x7f7fffffu)
-        codes_of<NS>(h, __uint_as_float(top), Q, code);
-    p.scales[at.dst * p.D + d] = scale_of(top, Q);
-    const int bytes = BITS == 8 ? p.N : (p.N + 1) / 2;
-    uint8_t* o = p.codes + (at.dst * p.D + d) * bytes;
-#pragma unroll
-    for (int i = 0; i < NS * BITS / 8; ++i)
-        if (i < bytes)
-            o[i] = static_cast<uint8_t>(BITS == 8 ? code[i]
-                                                  : (code[2 * i % NS] & 15) | code[(2 * i + 1) % NS] << 4);
 }
 
 template <int BITS>
@@ -218,27 +255,29 @@ __global__ void __launch_bounds__(kThreads) load_any_kernel(const StateParams p)
     Place at;
     if (!at.set(p))
         return;
-    const int64_t d = at.d0 + (threadIdx.x & 31);
     if (p.dst && slot_taken(p.dst, at.row, static_cast<int32_t>(at.dst), p.src, p.src_slots))
         return;
-    if (d >= p.D)
-        return;
     const int bytes = BITS == 8 ? p.N : (p.N + 1) / 2;
-    const uint8_t* c = p.codes + (at.src * p.D + d) * bytes;
-    const float scale = p.scales[at.src * p.D + d];
-    float* state = p.state_out + (at.dst * p.D + d) * p.N;
+    for (int j = 0; j < kChunks; ++j) {
+        const int64_t d = at.d0 + 32 * j + (threadIdx.x & 31);
+        if (d >= p.D)
+            return;
+        const uint8_t* c = p.codes + (at.src * p.D + d) * bytes;
+        const float scale = p.scales[at.src * p.D + d];
+        float* state = p.state_out + (at.dst * p.D + d) * p.N;
 #pragma unroll
-    for (int n = 0; n < SS_MAX_DSTATE; ++n)
-        if (n < p.N) {
-            const uint32_t v = c[n * BITS / 8] >> (BITS == 4 ? 4 * (n & 1) : 0);
-            state[n] = (static_cast<int>(v << (32 - BITS)) >> (32 - BITS)) * scale;
-        }
+        for (int n = 0; n < SS_MAX_DSTATE; ++n)
+            if (n < p.N) {
+                const uint32_t v = c[n * BITS / 8] >> (BITS == 4 ? 4 * (n & 1) : 0);
+                state[n] = (static_cast<int>(v << (32 - BITS)) >> (32 - BITS)) * scale;
+            }
+    }
 }
 
 template <int LPC, int BITS>
 cudaError_t launch(const StateParams& p, bool load, cudaStream_t st)
 {
-    const unsigned blocks = static_cast<unsigned>((p.D + kThreads - 1) / kThreads * p.rows);
+    const unsigned blocks = static_cast<unsigned>((p.D + kCtaChannels - 1) / kCtaChannels * p.rows);
     if (LPC == 0)
         load ? load_any_kernel<BITS><<<blocks, kThreads, 0, st>>>(p)
              : store_any_kernel<BITS><<<blocks, kThreads, 0, st>>>(p);

@@ -9,8 +9,9 @@
 // elementwise work done by every lane of a channel the kernel issued 293 instructions for 8 channels
 // and was bound by that: 72 us for 256 rows x 5120 channels x 16 states.)  Other N take one lane per
 // channel and 4-byte accesses, whose lines the next states of the same channels find in L1.  A CTA
-// keeps its channels' parameters (A alone is as long as a row's state) for up to kRows rows, one
-// row's loads ahead of the arithmetic.
+// keeps its channels' parameters (A alone is as long as a row's state) for up to kRows rows.  Measured
+// for those 256 rows: 42.1 us with 4 rows and 24 warps on an SM, 43.3 with 2 rows, 49 with 8; 51 us with
+// 16 warps and the next row's loads ahead of the arithmetic (70% of the measured HBM rate).
 #include "so_device.cuh"
 
 namespace so {
@@ -19,7 +20,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRows = 8;  // rows of a CTA at most
+constexpr int kRows = 4;  // rows of a CTA at most
 
 // What a row brings to a lane: the states of its cells, B and C of its state group, and the inputs
 // of its channel.
@@ -29,11 +30,15 @@ template <typename io_t, int LPC, int NS> struct Row {
     io_t u, delta, z, seen[SS_MAX_CONV_WIDTH - 1];
 };
 
-template <typename io_t, int LPC, bool VEC>
-__global__ void __launch_bounds__(kThreads) step_kernel(const StepParams p)
+// UNITS: N / 4, or 0 for an N that is no multiple of 4.
+template <typename io_t, int UNITS>
+__global__ void __launch_bounds__(kThreads, UNITS ? 6 : 3) step_kernel(const StepParams p)
 {
+    constexpr bool VEC = UNITS > 0;
+    constexpr int LPC = UNITS < 2 ? 1 : UNITS == 2 ? 2 : 4;
     constexpr int NS = VEC ? 4 : SS_MAX_DSTATE;  // states of a cell
     constexpr int CP = 32 / LPC;                 // channels of a pass
+    const int N = VEC ? 4 * UNITS : p.N;
     __shared__ int s_slot[kRows];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tiles = static_cast<int>((p.D + kThreads - 1) / kThreads);
@@ -42,7 +47,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepParams p)
     const int64_t d0 = static_cast<int64_t>(blockIdx.x % tiles) * kThreads + warp * 32;
     const int64_t d = d0 + lane;             // the lane's channel in elementwise work
     const int n0 = VEC ? 4 * (lane % LPC) : 0;
-    const int nn = VEC ? 4 : p.N;
+    const int nn = VEC ? 4 : N;
     const bool active = d < p.D;
     const int width = p.conv_width;
 
@@ -67,10 +72,10 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepParams p)
 #pragma unroll
     for (int s = 0; s < LPC; ++s) {
         const int64_t c = d0 + s * CP + lane / LPC;
-        holds[s] = c < p.D && n0 < p.N;
+        holds[s] = c < p.D && n0 < N;
 #pragma unroll
         for (int n = 0; n < NS; ++n)
-            A[s][n] = holds[s] && n < nn ? p.A[c * p.N + n0 + n] * kLog2e : 0.f;
+            A[s][n] = holds[s] && n < nn ? p.A[c * N + n0 + n] * kLog2e : 0.f;
     }
 #pragma unroll
     for (int j = 0; j < SS_MAX_CONV_WIDTH; ++j)
@@ -82,21 +87,20 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepParams p)
     }
     __syncthreads();
 
-    auto state_at = [&](int slot, int s) {
-        return p.state + (static_cast<int64_t>(slot) * p.D + d0 + s * CP + lane / LPC) * p.N + n0;
-    };
-    auto window_at = [&](int slot) {
-        return static_cast<io_t*>(p.conv_state) + static_cast<int64_t>(slot) * (width - 1) * p.D + d;
-    };
+    // the lane's first cell in slot 0, and the pitches of slots; a pass is CP * N floats further on
+    float* const cell0 = p.state + (d0 + lane / LPC) * N + n0;
+    const int64_t slot_pitch = p.D * N, window_pitch = p.D * (width - 1);
+    io_t* const window0 = static_cast<io_t*>(p.conv_state) + d;
+    const int64_t at0 = row0 * p.D + d;  // of [batch, D] tensors
     auto load = [&](int r, Row<io_t, LPC, NS>& x) {
-        const int slot = r < rows ? s_slot[r] : -1;
+        const int slot = s_slot[r];
         if (slot < 0)
             return;
-        const int64_t row = row0 + r;
+        const float* cell = cell0 + slot * slot_pitch;
 #pragma unroll
         for (int s = 0; s < LPC; ++s)
             if (holds[s]) {
-                const float* state = state_at(slot, s);
+                const float* state = cell + s * CP * N;
                 if (VEC) {
                     const float4 v = *reinterpret_cast<const float4*>(state);
                     x.h[s][0] = v.x, x.h[s][1] = v.y, x.h[s][2] = v.z, x.h[s][3] = v.w;
@@ -107,9 +111,9 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepParams p)
                             x.h[s][n] = state[n];
                 }
             }
-        if (n0 < p.N) {
-            const io_t* B = static_cast<const io_t*>(p.B) + row * p.N + n0;
-            const io_t* C = static_cast<const io_t*>(p.C) + row * p.N + n0;
+        if (n0 < N) {
+            const io_t* B = static_cast<const io_t*>(p.B) + (row0 + r) * N + n0;
+            const io_t* C = static_cast<const io_t*>(p.C) + (row0 + r) * N + n0;
             if (VEC) {
                 using raw = typename Pair<io_t>::raw;
 #pragma unroll
@@ -127,11 +131,12 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepParams p)
             }
         }
         if (active) {
-            x.u = static_cast<const io_t*>(p.u)[row * p.D + d];
-            x.delta = static_cast<const io_t*>(p.delta)[row * p.D + d];
+            const int64_t at = at0 + r * p.D;
+            x.u = static_cast<const io_t*>(p.u)[at];
+            x.delta = static_cast<const io_t*>(p.delta)[at];
             if (p.z)
-                x.z = static_cast<const io_t*>(p.z)[row * p.D + d];
-            const io_t* win = window_at(slot);
+                x.z = static_cast<const io_t*>(p.z)[at];
+            const io_t* win = window0 + slot * window_pitch;
 #pragma unroll
             for (int j = 0; j < SS_MAX_CONV_WIDTH - 1; ++j)
                 if (j < width - 1)
@@ -154,7 +159,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepParams p)
                 // (constant indices keep the taps in registers)
                 c = fmaf(width == 4 ? cw[3] : width == 3 ? cw[2] : width == 2 ? cw[1] : cw[0], u, c);
                 if (width > 1) {
-                    io_t* win = window_at(slot);
+                    io_t* win = window0 + slot * window_pitch;
 #pragma unroll
                     for (int j = 1; j < SS_MAX_CONV_WIDTH - 1; ++j)
                         if (j < width - 1)
@@ -171,10 +176,11 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepParams p)
         float B[NS], C[NS], y = 0.f;
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-            const bool used = n0 < p.N && n < nn;
+            const bool used = n0 < N && n < nn;
             B[n] = used ? ld1(&x.B[n]) : 0.f;
             C[n] = used ? ld1(&x.C[n]) : 0.f;
         }
+        float* cell = cell0 + slot * slot_pitch;
 #pragma unroll
         for (int s = 0; s < LPC; ++s) {
             // channel s * CP + lane / LPC of the warp, from the lane that has it
@@ -189,7 +195,7 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepParams p)
                         x.h[s][n] = fmaf(ex2(dl * A[s][n]), x.h[s][n], ws * B[n]);
                         part = fmaf(x.h[s][n], C[n], part);
                     }
-                float* state = state_at(slot, s);
+                float* state = cell + s * CP * N;
                 if (VEC) {
                     *reinterpret_cast<float4*>(state) =
                         make_float4(x.h[s][0], x.h[s][1], x.h[s][2], x.h[s][3]);
@@ -211,40 +217,35 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const StepParams p)
             y = fmaf(skip, u, y);
             if (p.z)
                 y *= silu_f(ld1(&x.z));
-            st1(static_cast<io_t*>(p.out) + (row0 + r) * p.D + d, y);
+            st1(static_cast<io_t*>(p.out) + at0 + r * p.D, y);
         }
     };
-    // slots of different rows are distinct, so a row's loads may pass the stores of the one before
-    Row<io_t, LPC, NS> x[2];
-    load(0, x[0]);
-    for (int r = 0; r < rows; r += 2) {
-        load(r + 1, x[1]);
-        step(r, x[0]);
-        if (r + 1 < rows) {
-            load(r + 2, x[0]);
-            step(r + 1, x[1]);
-        }
+    Row<io_t, LPC, NS> x;
+    for (int r = 0; r < rows; ++r) {
+        load(r, x);
+        step(r, x);
     }
 }
 
-template <typename io_t, int LPC, bool VEC> cudaError_t launch(StepParams p, cudaStream_t st)
+template <typename io_t, int UNITS> cudaError_t launch(StepParams p, cudaStream_t st)
 {
     const int64_t tiles = (p.D + kThreads - 1) / kThreads;
     // as many rows a CTA as still leave four CTAs for each of 148 SMs
     const int64_t rows = tiles * p.batch / (4 * 148);
     p.rows = static_cast<int>(rows < 1 ? 1 : rows > kRows ? kRows : rows);
     const int64_t blocks = tiles * ((p.batch + p.rows - 1) / p.rows);
-    step_kernel<io_t, LPC, VEC><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p);
+    step_kernel<io_t, UNITS><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(p);
     return cudaGetLastError();
 }
 
 template <typename io_t> cudaError_t launch_n(const StepParams& p, cudaStream_t st)
 {
     if (p.N % 4)
-        return launch<io_t, 1, false>(p, st);
-    return p.N == 4 ? launch<io_t, 1, true>(p, st)
-         : p.N == 8 ? launch<io_t, 2, true>(p, st)
-                    : launch<io_t, 4, true>(p, st);
+        return launch<io_t, 0>(p, st);
+    return p.N == 4    ? launch<io_t, 1>(p, st)
+           : p.N == 8  ? launch<io_t, 2>(p, st)
+           : p.N == 12 ? launch<io_t, 3>(p, st)
+                       : launch<io_t, 4>(p, st);
 }
 
 }  // namespace
