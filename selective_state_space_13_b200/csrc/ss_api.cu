@@ -247,8 +247,15 @@ ss_status selective_scan_fwd(const ss_shape* shape, const void* u, const void* d
         return SS_ERR_WORKSPACE;
 
     cudaStream_t strm = static_cast<cudaStream_t>(stream);
-    // the stream must belong to the current device, whose error word the kernels report to
+    // the stream must belong to the current device, whose error word the kernels report to; while
+    // it is being captured the runtime refuses to say (and asking would end the capture), so the
+    // launches themselves refuse a foreign stream then
     auto stream_on_current_device = [&]() -> ss_status {
+        cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+        if (cudaStreamIsCapturing(strm, &cap) != cudaSuccess)
+            return SS_ERR_CUDA;
+        if (cap != cudaStreamCaptureStatusNone)
+            return SS_OK;
         int dev = 0, sdev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess || cudaStreamGetDevice(strm, &sdev) != cudaSuccess)
             return SS_ERR_CUDA;

@@ -283,6 +283,9 @@ _ws_cache = {}
 
 def _workspace(nbytes, device):
     import torch
+    if torch.cuda.is_current_stream_capturing():
+        # a graph's scratch is its own: graphs may be replayed at the same time
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
     key = (device.index, torch.cuda.current_stream(device).cuda_stream)
     buf = _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:

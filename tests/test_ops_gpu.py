@@ -77,9 +77,10 @@ def test_recurrence_options(cuda_device, io, form, complement, reverse):
 
 @pytest.mark.parametrize("b,L,D", [(1, 1, 8), (3, 2, 8), (1, 31, 264), (2, 63, 128), (1, 65, 16),
                                    (1, 129, 1000), (5, 333, 200), (1, 5000, 8), (1, 1025, 520),
-                                   (33, 40, 136)])
+                                   (33, 40, 136), (1, 4200, 72), (2, 2049, 128)])
 @pytest.mark.parametrize("io", [F32, BF16])
 def test_recurrence_sizes(cuda_device, io, b, L, D):
+    # (few columns of many steps are cut into segments, from 8 clusters' rounds on)
     check_recurrence(rec_inputs(b + L + D, b, L, D, io, "sigmoid", initial=L % 2 == 1),
                      complement=True)
 
@@ -700,6 +701,37 @@ def test_captured_and_on_another_stream(cuda_device, name):
             graph.replay()
             for a, b in zip(out, want):
                 assert torch.equal(a, b)
+
+
+def test_forward_scan_and_training_step_captured(cuda_device):
+    # the forward scan under capture, alone and with its gradient as a whole training step
+    t = scan_inputs(194, 2, 200, 40, 16, BF16, dirs=(0, 1))
+    d = dict(zip(t, cuda(*t.values())))
+
+    def fwd():
+        return scan.selective_scan_fwd(d["u"], d["delta"], d["A"], d["B"], d["C"], D=d["D"], z=d["z"],
+                                       delta_bias=d["bias"], dirs=(0, 1), segments=3)
+
+    leaves = [d[n].clone().requires_grad_() for n in SCAN_NAMES]
+
+    def train():
+        out, last = ops.selective_scan(*leaves[:8], dirs=(0, 1), initial_state=leaves[8])
+        return list(torch.autograd.grad(out.float().square().sum() + last.sum(), leaves))
+
+    for call in (lambda: [fwd()], train):
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            want = [v.clone() for v in call()]
+        torch.cuda.current_stream().wait_stream(side)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = call()
+        for v in got:
+            v.zero_()
+        graph.replay()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
 
 
 def test_binding_refusals(cuda_device):
