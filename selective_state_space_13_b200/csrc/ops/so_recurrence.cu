@@ -6,23 +6,29 @@ namespace so {
 namespace {
 
 // out[d] = sum over rows of part[row, d], in a fixed order: 32 channels by 8 row groups a CTA.
-__global__ void __launch_bounds__(256) sum_rows_kernel(const float* part, float* out, int64_t rows,
-                                                       int64_t D)
+struct SumRows {
+    const float* part;
+    float* out;
+    int64_t rows, D;
+};
+
+__global__ void __launch_bounds__(256) sum_rows_kernel(const SumRows p)
 {
     __shared__ float s[8][33];
+    ss::pdl_wait();  // the launch before this one writes the rows
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int64_t d = blockIdx.x * int64_t{32} + x;
     float v = 0.f;
-    if (d < D)
-        for (int64_t r = y; r < rows; r += 8)
-            v += part[r * D + d];
+    if (d < p.D)
+        for (int64_t r = y; r < p.rows; r += 8)
+            v += p.part[r * p.D + d];
     s[y][x] = v;
     __syncthreads();
-    if (y == 0 && d < D) {
+    if (y == 0 && d < p.D) {
 #pragma unroll
         for (int i = 1; i < 8; ++i)
             v += s[i][x];
-        out[d] = v;
+        p.out[d] = v;
     }
 }
 
@@ -33,9 +39,8 @@ cudaError_t launch(const RecParams& p, bool backward, cudaStream_t st)
         return launch_cluster<io_t, FORM, COMP, false>(p, st);
     cudaError_t e = launch_cluster<io_t, FORM, COMP, true>(p, st);
     if (e == cudaSuccess && p.dbias) {
-        sum_rows_kernel<<<static_cast<unsigned>((p.D + 31) / 32), 256, 0, st>>>(
-            p.dbias_part, p.dbias, p.batch * p.S * p.cluster, p.D);
-        e = cudaGetLastError();
+        const SumRows s = {p.dbias_part, p.dbias, p.batch * p.S * p.cluster, p.D};
+        e = ss::launch_ex(sum_rows_kernel, static_cast<unsigned>((p.D + 31) / 32), 256, 0, st, true, s);
     }
     return e;
 }

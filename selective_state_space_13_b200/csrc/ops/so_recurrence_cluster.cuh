@@ -163,15 +163,6 @@ __global__ void __launch_bounds__(kRecThreads, 4)
     float2 carry = make_float2(0.f, 0.f);  // the state before this round (kept by warp 0)
     if (first && active)
         carry = make_float2(first[b * p.D + d], first[b * p.D + d + 1]);
-    // the segments' maps, and of an aggregate the product of the decays so far
-    float4* const seg_maps = p.seg_maps + static_cast<int64_t>(column) * p.S * 32 + lane;
-    float2 product = make_float2(1.f, 1.f);
-    if (p.aggregate)
-        carry = make_float2(0.f, 0.f);
-    else if (warp == 0)
-        for (int s = 0; s < seg; ++s)
-            carry = through(seg_maps[s * 32], carry);
-
     if (cs > 1) {
         if (threadIdx.x == 0) {
             ss::mbar_init(&sm.maps[0], 1);
@@ -217,6 +208,20 @@ __global__ void __launch_bounds__(kRecThreads, 4)
     load(0);
     if (!BWD)
         load(1);
+    // the maps of the segments before this one, which the launch before this one leaves (it may
+    // still be running until here); of an aggregate, the product of the decays so far
+    float4* const seg_maps = p.seg_maps + static_cast<int64_t>(column) * p.S * 32 + lane;
+    float2 product = make_float2(1.f, 1.f);
+    if (p.aggregate) {
+        carry = make_float2(0.f, 0.f);
+    } else if (p.S > 1) {
+        ss::pdl_wait();
+        if (warp == 0) {
+#pragma unroll 4
+            for (int s = 0; s < seg; ++s)
+                carry = through(seg_maps[s * 32], carry);
+        }
+    }
     bool waits = true;  // false once a wait has given up: the rest runs without waiting
     const float2 minus = make_float2(-1.f, -1.f);
     float2 db = make_float2(0.f, 0.f);  // -dbias
@@ -376,6 +381,7 @@ __global__ void __launch_bounds__(kRecThreads, 4)
                 make_float2(-db.x, -db.y);
         }
     }
+    ss::pdl_launch_dependents();
     if (cs > 1)
         cluster_meet();  // no CTA leaves while another may store to it
 }
@@ -394,12 +400,19 @@ cudaError_t launch_order(const RecParams& p, cudaStream_t st)
     cfg.blockDim = dim3(kRecThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = p.cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
     cfg.attrs = attr;
-    cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+    if (p.cluster > 1) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = p.cluster;
+        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
+    if (p.S > 1 && !p.aggregate) {  // it may start while the aggregates end
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++cfg.numAttrs;
+    }
     return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
