@@ -7,8 +7,14 @@
  * SS_ERR_DEVICE otherwise), arguments validated before anything is launched, base pointers of io
  * tensors and workspaces 16-byte aligned and dim * sizeof(io element) a multiple of 16.  Inputs
  * must not overlap outputs or the workspace.  A workspace belongs to one call until that call's
- * work is done; its contents on entry do not matter.  Every call can be captured into a CUDA
- * graph.  Results do not depend on the order in which blocks run: no floating-point atomics.
+ * work is done; its contents on entry do not matter.  Results do not depend on the order in which
+ * blocks run: no floating-point atomics.
+ *
+ * Every call can be captured into a CUDA graph, after a first call of its kind on the device (which
+ * loads the kernels and looks up the device error word); while a stream is captured its device is
+ * not checked.  gated_recurrence_fwd and gated_recurrence_bwd wait inside a kernel for the other
+ * blocks of a cluster; like every wait of the library these are bounded (2 s) and a wait that gives up is
+ * reported by selective_scan_device_status.
  */
 #ifndef SELECTIVE_SCAN_OPS_H
 #define SELECTIVE_SCAN_OPS_H

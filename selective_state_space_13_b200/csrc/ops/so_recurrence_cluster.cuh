@@ -23,8 +23,6 @@
 // than about three CTAs on an SM run slower, not faster.  TMA boxes for the rows: the same times.
 #pragma once
 
-#include <cuda.h>
-
 #include <type_traits>
 
 #include "so_device.cuh"
@@ -54,10 +52,9 @@ template <typename io_t, bool BWD> struct RecSmem {
     uint64_t maps[2];  // the maps of the cluster's CTAs have landed
 };
 
-// a - 1 of two gates (negative, so that it multiplies without a sign flip, which packed operations
-// would pay two instructions for).  `bias2` is the bias times log2(e): the sums are taken in base 2,
-// where the exponential is one instruction.  The sigmoid's 1 - a is sigmoid(-s), accurate in both
-// tails; s = -inf gives exp 0 and a - 1 = -1.
+// a - 1 of two gates.  `bias2` is the bias times log2(e): the sums are taken in base 2, where the
+// exponential is one instruction.  The sigmoid's 1 - a is sigmoid(-s), accurate in both tails; s =
+// -inf gives exp 0 and a - 1 = -1.
 template <int FORM, bool ACCURATE>
 __device__ __forceinline__ float2 decay_minus_one(float2 gate, float2 bias2)
 {
@@ -228,8 +225,10 @@ __global__ void __launch_bounds__(kRecThreads, 4)
     for (int m = 0; m < rounds; ++m) {
         const int st = m & 1;
         const int s0 = t0 + (m * cs + rank) * T::kRows + warp * N;  // this warp's first step
-        if (BWD)
-            load(m + 1);  // into the stage that the round before this one has used up
+        if (BWD) {
+            __syncwarp();  // every lane is through with the rows of the round before this one
+            load(m + 1);
+        }
         cp_wait_one();
         __syncwarp();
         // the thread's two channels of its step i, in tensor q

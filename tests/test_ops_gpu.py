@@ -282,11 +282,12 @@ def test_scan_bwd_optional_inputs(cuda_device):
     check_scan(t, flags=scan.SS_FLAG_GENERIC_A)
 
 
-def test_scan_bwd_extreme_steps(cuda_device):
+@pytest.mark.parametrize("io", [F32, BF16])
+def test_scan_bwd_extreme_steps(cuda_device, io):
     # steps that keep the state exactly (Delta = 0), steps that forget it, and zero inputs
-    t = scan_inputs(104, 2, 120, 16, 16, F32)
+    t = scan_inputs(104, 2, 120, 16, 16, io)
     r = torch.rand(t["delta"].shape, generator=gen(105))
-    t["delta"] = torch.where(r < 0.2, -200.0, torch.where(r > 0.8, 60.0, t["delta"]))
+    t["delta"] = torch.where(r < 0.2, -200.0, torch.where(r > 0.8, 60.0, t["delta"].float())).to(io)
     t["u"][:, 10:20] = 0
     t["z"][0, 5] = -90.0
     t["z"][0, 6] = 90.0
@@ -701,6 +702,103 @@ def test_captured_and_on_another_stream(cuda_device, name):
             graph.replay()
             for a, b in zip(out, want):
                 assert torch.equal(a, b)
+
+
+def test_two_calls_at_once(cuda_device):
+    # every operator on two streams, again and again without waiting: no call sees another's scratch
+    calls = operators()
+    want = {n: [v.clone() for v in c()] for n, c in calls.items() if n != "park"}
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(5):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got += [(n, calls[n]()) for n in want]
+    torch.cuda.synchronize()
+    for n, vs in got:
+        for a, b in zip(vs, want[n]):
+            assert torch.equal(a, b), n
+
+
+def guarded(like, fill=float("nan")):
+    """A tensor like `like` inside a larger buffer whose margins hold a canary: (view, buffer)."""
+    pad, n = 64, like.numel()
+    buf = torch.full((n + 2 * pad,), 93, dtype=like.dtype, device="cuda")
+    view = buf[pad:pad + n].view(like.shape)
+    view.fill_(fill if like.is_floating_point() else 0)
+    return view, buf
+
+
+def check_guards(bufs, whole=()):
+    for name, (view, buf) in bufs.items():
+        assert (buf[:64] == 93).all() and (buf[-64:] == 93).all(), name
+        if name in whole:
+            assert torch.isfinite(view.float()).all(), name
+
+
+@pytest.mark.parametrize("io", [F32, BF16])
+def test_outputs_stay_in_their_bounds(cuda_device, io):
+    # ragged sizes through the C entry points; every output element written, nothing beside them
+    lib, code = ops.load(), scan._io_code(io)
+    ref_, st = ops.ctypes.byref, torch.cuda.current_stream().cuda_stream
+    for b, L, D, reverse in ((2, 333, 136, 0), (1, 4201, 72, 1)):
+        r = rec_inputs(200 + L, b, L, D, io, "sigmoid")
+        e = dict(zip(r, cuda(*r.values())))
+        opts = ops.SsRecurrenceOpts(0, 1, reverse, 0)
+        sh = scan.make_shape(b, L, D, 1, code)
+        n = [ops.gated_recurrence_workspace_size(sh, opts, k) for k in (False, True)]
+        o = {"out": guarded(e["x"]), "last": guarded(e["initial_state"]), "dx": guarded(e["x"]),
+             "dgate": guarded(e["x"]), "dbias": guarded(e["gate_bias"]),
+             "dinit": guarded(e["initial_state"]),
+             "ws0": guarded(torch.zeros(n[0], dtype=torch.uint8)),
+             "ws1": guarded(torch.zeros(n[1], dtype=torch.uint8))}
+        p = {k: v[0].data_ptr() for k, v in o.items()}
+        x, gate, gb, h0, dout, dlast = (e[k].data_ptr() for k in ("x", "gate", "gate_bias",
+                                                                  "initial_state", "dout", "dlast"))
+        assert lib.gated_recurrence_fwd(ref_(sh), ref_(opts), x, gate, gb, h0, p["out"], p["last"],
+                                        p["ws0"], n[0], st) == 0
+        assert lib.gated_recurrence_bwd(ref_(sh), ref_(opts), x, gate, gb, h0, p["out"], dout, dlast,
+                                        p["dx"], p["dgate"], p["dbias"], p["dinit"], p["ws1"], n[1],
+                                        st) == 0
+        torch.cuda.synchronize()
+        check_guards(o, ("out", "last", "dx", "dgate", "dbias", "dinit"))
+    for dirs, H, W, L, segs in (((0,), 0, 0, 77, 3), ((0, 2, 1, 3), 7, 9, 63, 2)):
+        t = scan_inputs(210 + L, 2, L, 136, 11, io, dirs=dirs)
+        d = dict(zip(t, cuda(*t.values())))
+        sh, dm = scan.make_shape(2, L, 136, 11, code), scan.make_dirmap(dirs, H, W)
+        op = scan.make_opts(segs, 0, None, d["h0"].data_ptr())
+        n = ops.selective_scan_bwd_workspace_size(sh, dm, op)
+        names = ("u", "delta", "A", "B", "C", "D", "z", "bias", "h0")
+        o = {k: guarded(d[k]) for k in names}
+        o["ws"] = guarded(torch.zeros(n, dtype=torch.uint8))
+        g = ops.SsScanGrads(*(o[k][0].data_ptr() for k in names))
+        q = {k: v.data_ptr() for k, v in d.items()}
+        assert lib.selective_scan_bwd(
+            ref_(sh), q["u"], q["delta"], q["A"], q["B"], q["C"], q["D"], q["z"], q["bias"], 1,
+            ref_(dm), q["dout"], q["dlast"], ref_(g), o["ws"][0].data_ptr(), n, st, ref_(op)) == 0
+        torch.cuda.synchronize()
+        check_guards(o, names)
+    for N in (16, 12, 5):
+        s = step_inputs(220 + N, 3, 136, N, io, width=4, slots=4)
+        f = dict(zip(s, cuda(*s.values())))
+        o = {"out": guarded(f["u"]), "state": guarded(f["state"]), "cs": guarded(f["cs"])}
+        o["state"][0].copy_(f["state"])
+        o["cs"][0].copy_(f["cs"])
+        slots = torch.tensor([3, 0, 2], dtype=torch.int32, device="cuda")
+        ops.selective_scan_step(f["u"], f["delta"], f["A"], f["B"], f["C"], o["state"][0], D=f["D"],
+                                z=f["z"], delta_bias=f["bias"], slots=slots, conv_weight=f["cw"],
+                                conv_bias=f["cb"], conv_state=o["cs"][0], out=o["out"][0])
+        for bits in (8, 4):
+            width = N if bits == 8 else (N + 1) // 2
+            o["codes%d" % bits] = guarded(torch.zeros(4, 136, width, dtype=torch.int8))
+            o["scales%d" % bits] = guarded(torch.zeros(4, 136))
+            o["back%d" % bits] = guarded(f["state"])
+            args = (o["codes%d" % bits][0], o["scales%d" % bits][0])
+            ops.selective_state_store(o["state"][0], *args, bits=bits)
+            ops.selective_state_load(*args, o["back%d" % bits][0], bits=bits)
+        torch.cuda.synchronize()
+        check_guards(o, ("out", "state", "cs", "scales8", "back8", "scales4", "back4"))
 
 
 def test_forward_scan_and_training_step_captured(cuda_device):
