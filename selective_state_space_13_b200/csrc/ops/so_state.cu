@@ -2,7 +2,8 @@
 // one fp32 scale.  Both directions move bytes and nothing else, so HBM bounds them.  A warp has 32
 // channels of a row; where N is a multiple of 4, LPC lanes share a channel with 16-byte state
 // accesses in LPC passes (as in the step), and what belongs to a whole channel -- the scale, and in
-// the load its codes, 16 bytes for 16 states -- is one lane's; other N take one lane per channel.
+// the load its codes, 16 bytes for 16 states -- is one lane's; with other N a lane has its channel's
+// states and codes from shared memory, through which the warp moves them in contiguous pieces.
 //
 // round(h q / amax) is what fp32 arithmetic gives wherever its error (below 2^-21 q) cannot move
 // the value across the border between two codes; next to a border the quotient is taken again in
@@ -212,65 +213,97 @@ __global__ void __launch_bounds__(kThreads) load_kernel(const StateParams p)
     }
 }
 
-// Any other N: one lane per channel.
-template <int BITS>
+// n words between memory and shared memory, by a warp, several at a time where both ends allow it.
+template <typename word_t, typename wide_t>
+__device__ __forceinline__ void move(word_t* dst, const word_t* src, int n, bool wide)
+{
+    constexpr int W = sizeof(wide_t) / sizeof(word_t);
+    const int lane = threadIdx.x & 31;
+    if (wide)
+        for (int i = lane; i < n / W; i += 32)
+            reinterpret_cast<wide_t*>(dst)[i] = reinterpret_cast<const wide_t*>(src)[i];
+    else
+        for (int i = lane; i < n; i += 32)
+            dst[i] = src[i];
+}
+
+// Any other N, at most NS: one lane per channel.
+template <int BITS, int NS>
 __global__ void __launch_bounds__(kThreads) store_any_kernel(const StateParams p)
 {
-    constexpr int Q = BITS == 8 ? 127 : 7, NS = SS_MAX_DSTATE;
+    constexpr int Q = BITS == 8 ? 127 : 7;
+    __shared__ __align__(16) float s_state[kWarps][32 * NS];
+    __shared__ __align__(16) uint8_t s_codes[kWarps][32 * NS];
     Place at;
     if (!at.set(p))
         return;
     if (p.dst && slot_taken(p.dst, at.row, static_cast<int32_t>(at.dst), p.src, p.src_slots))
         return;
-    for (int j = 0; j < kChunks; ++j) {
-        const int64_t d = at.d0 + 32 * j + (threadIdx.x & 31);
-        if (d >= p.D)
-            return;
-        const float* state = p.state_in + (at.src * p.D + d) * p.N;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, N = p.N;
+    const int bytes = BITS == 8 ? N : (N + 1) / 2;
+    // whole rows start on 16-byte (codes: 4-byte) borders; 32 channels always are a multiple of both
+    const bool wide = p.D * N % 4 == 0, wide_codes = p.D * bytes % 4 == 0;
+    for (int j = 0; j < kChunks && at.d0 < p.D; ++j, at.d0 += 32) {
+        const int count = static_cast<int>(p.D - at.d0 < 32 ? p.D - at.d0 : 32);
+        move<float, float4>(s_state[warp], p.state_in + (at.src * p.D + at.d0) * N, count * N, wide);
+        __syncwarp();
         float h[NS];
         unsigned top = 0;
         uint32_t code[NS];
 #pragma unroll
         for (int n = 0; n < NS; ++n) {
-            h[n] = n < p.N ? state[n] : 0.f;
+            h[n] = n < N && lane < count ? s_state[warp][lane * N + n] : 0.f;
             top = max(top, __float_as_uint(h[n]) & 0x7fffffffu);
             code[n] = 0;
         }
         if (top - 1 < 0x7f7fffffu)
             codes_of<NS>(h, __uint_as_float(top), Q, code);
-        p.scales[at.dst * p.D + d] = scale_of(top, Q);
-        const int bytes = BITS == 8 ? p.N : (p.N + 1) / 2;
-        uint8_t* o = p.codes + (at.dst * p.D + d) * bytes;
+        if (lane < count) {
+            p.scales[at.dst * p.D + at.d0 + lane] = scale_of(top, Q);
 #pragma unroll
-        for (int i = 0; i < NS * BITS / 8; ++i)
-            if (i < bytes)
-                o[i] = static_cast<uint8_t>(
-                    BITS == 8 ? code[i] : (code[2 * i % NS] & 15) | code[(2 * i + 1) % NS] << 4);
+            for (int i = 0; i < NS * BITS / 8; ++i)
+                if (i < bytes)
+                    s_codes[warp][lane * bytes + i] = static_cast<uint8_t>(
+                        BITS == 8 ? code[i] : (code[2 * i % NS] & 15) | code[(2 * i + 1) % NS] << 4);
+        }
+        __syncwarp();
+        move<uint8_t, uint32_t>(p.codes + (at.dst * p.D + at.d0) * bytes, s_codes[warp], count * bytes,
+                                wide_codes);
+        __syncwarp();
     }
 }
 
-template <int BITS>
+template <int BITS, int NS>
 __global__ void __launch_bounds__(kThreads) load_any_kernel(const StateParams p)
 {
+    __shared__ __align__(16) float s_state[kWarps][32 * NS];
+    __shared__ __align__(16) uint8_t s_codes[kWarps][32 * NS];
     Place at;
     if (!at.set(p))
         return;
     if (p.dst && slot_taken(p.dst, at.row, static_cast<int32_t>(at.dst), p.src, p.src_slots))
         return;
-    const int bytes = BITS == 8 ? p.N : (p.N + 1) / 2;
-    for (int j = 0; j < kChunks; ++j) {
-        const int64_t d = at.d0 + 32 * j + (threadIdx.x & 31);
-        if (d >= p.D)
-            return;
-        const uint8_t* c = p.codes + (at.src * p.D + d) * bytes;
-        const float scale = p.scales[at.src * p.D + d];
-        float* state = p.state_out + (at.dst * p.D + d) * p.N;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, N = p.N;
+    const int bytes = BITS == 8 ? N : (N + 1) / 2;
+    const bool wide = p.D * N % 4 == 0, wide_codes = p.D * bytes % 4 == 0;
+    for (int j = 0; j < kChunks && at.d0 < p.D; ++j, at.d0 += 32) {
+        const int count = static_cast<int>(p.D - at.d0 < 32 ? p.D - at.d0 : 32);
+        move<uint8_t, uint32_t>(s_codes[warp], p.codes + (at.src * p.D + at.d0) * bytes, count * bytes,
+                                wide_codes);
+        const float scale = lane < count ? p.scales[at.src * p.D + at.d0 + lane] : 0.f;
+        __syncwarp();
+        if (lane < count) {
 #pragma unroll
-        for (int n = 0; n < SS_MAX_DSTATE; ++n)
-            if (n < p.N) {
-                const uint32_t v = c[n * BITS / 8] >> (BITS == 4 ? 4 * (n & 1) : 0);
-                state[n] = (static_cast<int>(v << (32 - BITS)) >> (32 - BITS)) * scale;
-            }
+            for (int n = 0; n < NS; ++n)
+                if (n < N) {
+                    const uint32_t v = s_codes[warp][lane * bytes + n * BITS / 8] >>
+                                       (BITS == 4 ? 4 * (n & 1) : 0);
+                    s_state[warp][lane * N + n] = (static_cast<int>(v << (32 - BITS)) >> (32 - BITS)) * scale;
+                }
+        }
+        __syncwarp();
+        move<float, float4>(p.state_out + (at.dst * p.D + at.d0) * N, s_state[warp], count * N, wide);
+        __syncwarp();
     }
 }
 
@@ -278,19 +311,25 @@ template <int LPC, int BITS>
 cudaError_t launch(const StateParams& p, bool load, cudaStream_t st)
 {
     const unsigned blocks = static_cast<unsigned>((p.D + kCtaChannels - 1) / kCtaChannels * p.rows);
-    if (LPC == 0)
-        load ? load_any_kernel<BITS><<<blocks, kThreads, 0, st>>>(p)
-             : store_any_kernel<BITS><<<blocks, kThreads, 0, st>>>(p);
-    else
-        load ? load_kernel<LPC ? LPC : 1, BITS><<<blocks, kThreads, 0, st>>>(p)
-             : store_kernel<LPC ? LPC : 1, BITS><<<blocks, kThreads, 0, st>>>(p);
+    load ? load_kernel<LPC, BITS><<<blocks, kThreads, 0, st>>>(p)
+         : store_kernel<LPC, BITS><<<blocks, kThreads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <int BITS, int NS>
+cudaError_t launch_any(const StateParams& p, bool load, cudaStream_t st)
+{
+    const unsigned blocks = static_cast<unsigned>((p.D + kCtaChannels - 1) / kCtaChannels * p.rows);
+    load ? load_any_kernel<BITS, NS><<<blocks, kThreads, 0, st>>>(p)
+         : store_any_kernel<BITS, NS><<<blocks, kThreads, 0, st>>>(p);
     return cudaGetLastError();
 }
 
 template <int BITS> cudaError_t launch_n(const StateParams& p, bool load, cudaStream_t st)
 {
     if (p.N % 4)
-        return launch<0, BITS>(p, load, st);
+        return p.N < 8 ? launch_any<BITS, 8>(p, load, st)
+                       : launch_any<BITS, SS_MAX_DSTATE>(p, load, st);
     return p.N == 4 ? launch<1, BITS>(p, load, st)
          : p.N == 8 ? launch<2, BITS>(p, load, st)
                     : launch<4, BITS>(p, load, st);

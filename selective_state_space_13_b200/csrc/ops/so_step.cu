@@ -7,8 +7,9 @@
 // passes over 32 / LPC channels each, so that every access of a warp is contiguous; Delta and
 // Delta u come to the lanes of a channel by shuffle and y goes back the same way.  (With the
 // elementwise work done by every lane of a channel the kernel issued 293 instructions for 8 channels
-// and was bound by that: 72 us for 256 rows x 5120 channels x 16 states.)  Other N take one lane per
-// channel and 4-byte accesses, whose lines the next states of the same channels find in L1.  A CTA
+// and was bound by that: 72 us for 256 rows x 5120 channels x 16 states.)  With other N a lane
+// has all states of its channel; they, and B and C, pass through shared memory, so that the accesses
+// to memory are contiguous there too (directly: N = 15, 111 us for those rows).  A CTA
 // keeps its channels' parameters (A alone is as long as a row's state) for up to kRows rows.  Measured
 // for those 256 rows: 42.1 us with 4 rows and 24 warps on an SM, 43.3 with 2 rows, 49 with 8; 51 us with
 // 16 warps and the next row's loads ahead of the arithmetic (70% of the measured HBM rate).
@@ -26,20 +27,23 @@ constexpr int kRows = 4;  // rows of a CTA at most
 // of its channel.
 template <typename io_t, int LPC, int NS> struct Row {
     float h[LPC][NS];
-    alignas(8) io_t B[NS], C[NS];
+    alignas(8) io_t B[4], C[4];  // (N a multiple of 4)
     io_t u, delta, z, seen[SS_MAX_CONV_WIDTH - 1];
 };
 
-// UNITS: N / 4, or 0 for an N that is no multiple of 4.
+// UNITS: N / 4, or for an N that is no multiple of 4 the states to make room for, negative.
 template <typename io_t, int UNITS>
-__global__ void __launch_bounds__(kThreads, UNITS ? 6 : 3) step_kernel(const StepParams p)
+__global__ void __launch_bounds__(kThreads, UNITS > 0 ? 6 : 3) step_kernel(const StepParams p)
 {
     constexpr bool VEC = UNITS > 0;
     constexpr int LPC = UNITS < 2 ? 1 : UNITS == 2 ? 2 : 4;
-    constexpr int NS = VEC ? 4 : SS_MAX_DSTATE;  // states of a cell
+    constexpr int NS = VEC ? 4 : -UNITS;  // states of a cell
     constexpr int CP = 32 / LPC;                 // channels of a pass
     const int N = VEC ? 4 * UNITS : p.N;
     __shared__ int s_slot[kRows];
+    // other N: a warp's states, and B and C of its row
+    __shared__ __align__(16) float s_cell[VEC ? 1 : kWarps][VEC ? 4 : 32 * NS];
+    __shared__ __align__(16) float s_bc[VEC ? 1 : kWarps][VEC ? 4 : 2 * SS_MAX_DSTATE];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int tiles = static_cast<int>((p.D + kThreads - 1) / kThreads);
     const int64_t row0 = static_cast<int64_t>(blockIdx.x / tiles) * p.rows;
@@ -92,43 +96,47 @@ __global__ void __launch_bounds__(kThreads, UNITS ? 6 : 3) step_kernel(const Ste
     const int64_t slot_pitch = p.D * N, window_pitch = p.D * (width - 1);
     io_t* const window0 = static_cast<io_t*>(p.conv_state) + d;
     const int64_t at0 = row0 * p.D + d;  // of [batch, D] tensors
+    // other N: the warp's states of a slot as 16-byte pieces (D, and so D * N, is a multiple of 4)
+    const int pieces = d0 < p.D ? static_cast<int>(p.D - d0 < 32 ? p.D - d0 : 32) * N / 4 : 0;
+    float4* const slot0 = reinterpret_cast<float4*>(p.state + d0 * N);
+    float4* const staged = reinterpret_cast<float4*>(s_cell[VEC ? 0 : warp]);
     auto load = [&](int r, Row<io_t, LPC, NS>& x) {
         const int slot = s_slot[r];
         if (slot < 0)
             return;
-        const float* cell = cell0 + slot * slot_pitch;
+        const io_t* B = static_cast<const io_t*>(p.B) + (row0 + r) * N + n0;
+        const io_t* C = static_cast<const io_t*>(p.C) + (row0 + r) * N + n0;
+        if (VEC) {
+            const float* cell = cell0 + slot * slot_pitch;
 #pragma unroll
-        for (int s = 0; s < LPC; ++s)
-            if (holds[s]) {
-                const float* state = cell + s * CP * N;
-                if (VEC) {
-                    const float4 v = *reinterpret_cast<const float4*>(state);
+            for (int s = 0; s < LPC; ++s)
+                if (holds[s]) {
+                    const float4 v = *reinterpret_cast<const float4*>(cell + s * CP * N);
                     x.h[s][0] = v.x, x.h[s][1] = v.y, x.h[s][2] = v.z, x.h[s][3] = v.w;
-                } else {
-#pragma unroll
-                    for (int n = 0; n < NS; ++n)
-                        if (n < nn)
-                            x.h[s][n] = state[n];
                 }
-            }
-        if (n0 < N) {
-            const io_t* B = static_cast<const io_t*>(p.B) + (row0 + r) * N + n0;
-            const io_t* C = static_cast<const io_t*>(p.C) + (row0 + r) * N + n0;
-            if (VEC) {
+            if (n0 < N) {
                 using raw = typename Pair<io_t>::raw;
 #pragma unroll
                 for (int n = 0; n < 4; n += 2) {
                     *reinterpret_cast<raw*>(&x.B[n]) = *reinterpret_cast<const raw*>(B + n);
                     *reinterpret_cast<raw*>(&x.C[n]) = *reinterpret_cast<const raw*>(C + n);
                 }
-            } else {
-#pragma unroll
-                for (int n = 0; n < NS; ++n)
-                    if (n < nn) {
-                        x.B[n] = B[n];
-                        x.C[n] = C[n];
-                    }
             }
+        } else {
+            const float4* from = slot0 + slot * slot_pitch / 4;
+            float4 v[NS / 4];
+#pragma unroll
+            for (int i = 0; i < NS / 4; ++i)
+                if (lane + 32 * i < pieces)
+                    v[i] = from[lane + 32 * i];
+            const int n = lane % SS_MAX_DSTATE;
+            const float bc = n < N ? ld1((lane < SS_MAX_DSTATE ? B : C) + n) : 0.f;
+            __syncwarp();  // the row before this one is done with the staged values
+#pragma unroll
+            for (int i = 0; i < NS / 4; ++i)
+                if (lane + 32 * i < pieces)
+                    staged[lane + 32 * i] = v[i];
+            s_bc[VEC ? 0 : warp][lane] = bc;
         }
         if (active) {
             const int64_t at = at0 + r * p.D;
@@ -174,11 +182,20 @@ __global__ void __launch_bounds__(kThreads, UNITS ? 6 : 3) step_kernel(const Ste
         }
         const float w = delta * u;
         float B[NS], C[NS], y = 0.f;
+        if (VEC) {
 #pragma unroll
-        for (int n = 0; n < NS; ++n) {
-            const bool used = n0 < N && n < nn;
-            B[n] = used ? ld1(&x.B[n]) : 0.f;
-            C[n] = used ? ld1(&x.C[n]) : 0.f;
+            for (int n = 0; n < NS; ++n) {
+                B[n] = n0 < N ? ld1(&x.B[n % 4]) : 0.f;
+                C[n] = n0 < N ? ld1(&x.C[n % 4]) : 0.f;
+            }
+        } else {
+            __syncwarp();
+#pragma unroll
+            for (int n = 0; n < NS; ++n) {
+                x.h[0][n] = n < nn && active ? s_cell[VEC ? 0 : warp][lane * N + n] : 0.f;
+                B[n] = s_bc[VEC ? 0 : warp][n % (2 * SS_MAX_DSTATE)];
+                C[n] = s_bc[VEC ? 0 : warp][(SS_MAX_DSTATE + n) % (2 * SS_MAX_DSTATE)];
+            }
         }
         float* cell = cell0 + slot * slot_pitch;
 #pragma unroll
@@ -195,15 +212,14 @@ __global__ void __launch_bounds__(kThreads, UNITS ? 6 : 3) step_kernel(const Ste
                         x.h[s][n] = fmaf(ex2(dl * A[s][n]), x.h[s][n], ws * B[n]);
                         part = fmaf(x.h[s][n], C[n], part);
                     }
-                float* state = cell + s * CP * N;
                 if (VEC) {
-                    *reinterpret_cast<float4*>(state) =
+                    *reinterpret_cast<float4*>(cell + s * CP * N) =
                         make_float4(x.h[s][0], x.h[s][1], x.h[s][2], x.h[s][3]);
                 } else {
 #pragma unroll
                     for (int n = 0; n < NS; ++n)
                         if (n < nn)
-                            state[n] = x.h[s][n];
+                            s_cell[VEC ? 0 : warp][lane * N + n] = x.h[s][n];
                 }
             }
 #pragma unroll
@@ -212,6 +228,14 @@ __global__ void __launch_bounds__(kThreads, UNITS ? 6 : 3) step_kernel(const Ste
             // back to the lane of the channel: lane l belongs to pass l / CP
             const float mine = LPC > 1 ? __shfl_sync(0xffffffffu, part, (lane % CP) * LPC) : part;
             y = lane / CP == s ? mine : y;
+        }
+        if (!VEC) {
+            __syncwarp();
+            float4* to = slot0 + slot * slot_pitch / 4;
+#pragma unroll
+            for (int i = 0; i < NS / 4; ++i)
+                if (lane + 32 * i < pieces)
+                    to[lane + 32 * i] = staged[lane + 32 * i];
         }
         if (active) {
             y = fmaf(skip, u, y);
@@ -241,7 +265,7 @@ template <typename io_t, int UNITS> cudaError_t launch(StepParams p, cudaStream_
 template <typename io_t> cudaError_t launch_n(const StepParams& p, cudaStream_t st)
 {
     if (p.N % 4)
-        return launch<io_t, 0>(p, st);
+        return p.N < 8 ? launch<io_t, -8>(p, st) : launch<io_t, -SS_MAX_DSTATE>(p, st);
     return p.N == 4    ? launch<io_t, 1>(p, st)
            : p.N == 8  ? launch<io_t, 2>(p, st)
            : p.N == 12 ? launch<io_t, 3>(p, st)
