@@ -216,7 +216,8 @@ ss_status plan_bwd(const ss_shape* s, const ss_direction_map* dmap, const ss_lau
         want = o->segments;
     }
     const int64_t L = s->seqlen, rows = s->batch * pl->K;
-    const int64_t ctiles = ceil_div(s->dim, so::kBwdChannels), ntiles = ceil_div(L, so::kBwdTile);
+    const int64_t states = s->dstate > 8 ? 16 : 8;  // as the kernels pad them
+    const int64_t ctiles = ceil_div(s->dim, so::kBwdCells / states), ntiles = ceil_div(L, so::kBwdTile);
     const int64_t units = rows * ctiles;
     if (want == 0)
         want = bwd_segments(units, L);
@@ -241,16 +242,16 @@ ss_status plan_bwd(const ss_shape* s, const ss_direction_map* dmap, const ss_lau
         return at;
     };
     const size_t R = static_cast<size_t>(rows), D = static_cast<size_t>(s->dim);
-    pl->off_ckpt = take(R * ntiles * ctiles * so::kBwdChannels * 16);
+    pl->off_ckpt = take(R * ntiles * ctiles * so::kBwdCells);
     if (pl->split) {
         pl->off_cum = take(R * ntiles * D);
-        const size_t cells = R * pl->S * ctiles * so::kBwdChannels * 16;
+        const size_t cells = R * pl->S * ctiles * so::kBwdCells;
         pl->off_h = take(cells);
         pl->off_p = take(cells);
         pl->off_g = take(cells);
     }
-    pl->off_dbc = take(R * ctiles * L * 32);
-    pl->off_dpar = take(R * pl->S * D * 18);
+    pl->off_dbc = take(R * ctiles * L * 2 * states);
+    pl->off_dpar = take(R * pl->S * D * (states + 2));
     if (pl->K > 1) {
         const size_t plane = R * L * D;
         if (!(pl->flags & SS_FLAG_U_PER_DIRECTION))
@@ -514,8 +515,10 @@ ss_status selective_scan_bwd(const ss_shape* shape, const void* u, const void* d
     p.H = pl.H;
     p.W = pl.W;
     p.softplus = softplus ? 1 : 0;
-    return status_of(shape->io_dtype == SS_BF16 ? so::launch_scan_bwd_bf16(p, strm)
-                                                : so::launch_scan_bwd_f32(p, strm));
+    if (shape->io_dtype == SS_BF16)
+        return status_of(N > 8 ? so::launch_scan_bwd_bf16_4(p, strm)
+                               : so::launch_scan_bwd_bf16_2(p, strm));
+    return status_of(N > 8 ? so::launch_scan_bwd_f32_4(p, strm) : so::launch_scan_bwd_f32_2(p, strm));
 }
 
 ss_status selective_scan_step(const ss_shape* shape, int64_t num_slots, const void* u,

@@ -50,11 +50,11 @@ struct BwdParams {
     ss_scan_grads g;
     float* ckpt;      // states at the start of every slice, from the segment start (thread order)
     float* cum;       // [K*batch, slices, D] Delta summed from the segment start (SPLIT)
-    float* seg_h;     // [K*batch, S, D padded, 16] end state of a segment scanned from zero
+    float* seg_h;     // [K*batch, S, cells] end state of a segment scanned from zero
     float* seg_p;     // the same shape: product of Abar over the segment
     float* seg_g;     // the same shape: gradient that a zero-ended segment hands to the one before
-    float* dbc;       // [K*batch, channel tiles, L, 2, 16] partial sums of dB and dC
-    float* dpar;      // [K*batch*S, D, 18] partial sums of dA, dDskip, ddelta_bias
+    float* dbc;       // [K*batch, channel tiles, L, 2, states padded] partial sums of dB and dC
+    float* dpar;      // [K*batch*S, D, states padded + 2] partial sums of dA, dDskip, ddelta_bias
     float* du_part;   // [K, batch, L, D] (several directions share u)
     float* dz_part;   // [K, batch, L, D] (several directions with a gate)
     int64_t batch, L, D, seg_len;
@@ -65,11 +65,13 @@ struct BwdParams {
 };
 
 constexpr int kBwdTile = 4;       // steps of a slice: one checkpoint each
-constexpr int kBwdChannels = 64;  // channels of a CTA
+constexpr int kBwdCells = 1024;   // (channel, state) cells of a CTA, states padded to 8 or 16
 
-// One translation unit per io type.
-cudaError_t launch_scan_bwd_f32(const BwdParams& p, cudaStream_t st);
-cudaError_t launch_scan_bwd_bf16(const BwdParams& p, cudaStream_t st);
+// One translation unit per io type and number of groups of 4 states (2: N up to 8, 4: up to 16).
+cudaError_t launch_scan_bwd_f32_2(const BwdParams& p, cudaStream_t st);
+cudaError_t launch_scan_bwd_f32_4(const BwdParams& p, cudaStream_t st);
+cudaError_t launch_scan_bwd_bf16_2(const BwdParams& p, cudaStream_t st);
+cudaError_t launch_scan_bwd_bf16_4(const BwdParams& p, cudaStream_t st);
 
 // ---------------------------------------------------------------- single-token step
 

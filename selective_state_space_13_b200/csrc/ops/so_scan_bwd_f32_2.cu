@@ -1,0 +1,12 @@
+// Gradient of the selective scan for float io and N up to 8.
+#define SO_STATE_GROUPS 2
+#include "so_scan_bwd_kernels.cuh"
+
+namespace so {
+
+cudaError_t launch_scan_bwd_f32_2(const BwdParams& p, cudaStream_t st)
+{
+    return launch_bwd_io<float>(p, st);
+}
+
+}  // namespace so

@@ -6,7 +6,8 @@
 // recurrence over them.  Nothing of size batch x L x D x N crosses HBM except one state in kT.
 //
 // A CTA of 4 warps owns 64 channels of one (direction, batch row, segment), a warp 16 of them, a
-// thread 2 adjacent channels x 4 states: 4 lanes make a channel.  The two channels are the halves
+// thread 2 adjacent channels x 4 states: 4 lanes make a channel (for N up to 8: 128, 32, and 2 lanes;
+// SO_STATE_GROUPS says which, one translation unit each).  The two channels are the halves
 // of every packed f32x2 operation, so Delta, Delta u and dy come out of shared memory as pairs and
 // B and C as duplicated pairs, with no moves to build operands.  The sums over states (y, sum g B,
 // sum g A h) and over channels (dB, dC) go through shared memory that is private to the warp: a
@@ -37,18 +38,20 @@ namespace so {
 
 namespace {
 
-constexpr int kT = kBwdTile;      // steps of a slice
-constexpr int kTL = 2 * kT;       // steps of a tile: what is loaded and prepared together
-constexpr int kC = kBwdChannels;  // channels of a CTA
+constexpr int kG = SO_STATE_GROUPS;    // groups of 4 states: 4 (N up to 16) or 2 (N up to 8)
+constexpr int kNP = 4 * kG;            // states, padded
+constexpr int kT = kBwdTile;           // steps of a slice
+constexpr int kTL = 2 * kT;            // steps of a tile: what is loaded and prepared together
 constexpr int kWarps = 4;
 constexpr int kBwdThreads = 32 * kWarps;
-constexpr int kWC = kC / kWarps;  // channels of a warp
-constexpr int kNP = 16;           // states, padded
-// row pitch of raw tiles: the 4 steps x 8 channel pairs that a warp reads together lie in
+constexpr int kWC = 64 / kG;           // channels of a warp
+constexpr int kC = kWC * kWarps;       // channels of a CTA
+// pitches of raw rows and of the partial sums of a step: what a warp reads together lies in
 // different banks
-constexpr int kPitch = kC + 16;
-constexpr int kPartPitch = 4 * kWC + 8;  // likewise for the partial sums of a step
-static_assert(kT == 4 && kWC == 16, "lane = 4 * (channel pair) + (state group or step of a slice)");
+constexpr int kPitch = kC + 64 / kG;
+constexpr int kPartPitch = kG * kWC + 32 / kG;
+static_assert((kG == 2 || kG == 4) && kT == 4, "lane = kG * (channel pair) + state group");
+static_assert(kC == kBwdCells / kNP, "the host's plan counts the same channels");
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p)
 {
@@ -198,8 +201,7 @@ __device__ __forceinline__ void fill_cta(const BwdParams& p, const Unit& un, Cta
 
 // Starts the copies of the tile of steps t..t+kTL-1 into a stage; returns the raw B and C elements
 // that this thread will convert.
-constexpr int kBC = kTL * kNP / kBwdThreads;
-static_assert(kBC * kBwdThreads == kTL * kNP, "whole rounds of B and C elements");
+constexpr int kBC = (kTL * kNP + kBwdThreads - 1) / kBwdThreads;
 
 template <typename io_t>
 __device__ __forceinline__ void issue(const BwdParams& p, const Unit& un, const Cta& cta, int t,
@@ -234,7 +236,7 @@ __device__ __forceinline__ void issue(const BwdParams& p, const Unit& un, const 
 #pragma unroll
     for (int i = 0; i < kBC; ++i) {
         const int j = threadIdx.x + i * kBwdThreads, r = j / kNP, n = j % kNP;
-        const bool ok = r < rows && n < p.N;
+        const bool ok = j < kTL * kNP && r < rows && n < p.N;
         const int64_t at = static_cast<int64_t>(t + r) * p.N + n;
         bc[i][0] = ok ? gB[at] : io_t(0.f);
         bc[i][1] = ok ? gC[at] : io_t(0.f);
@@ -242,7 +244,7 @@ __device__ __forceinline__ void issue(const BwdParams& p, const Unit& un, const 
 }
 
 // The thread's place: channels c, c+1 of the CTA, states 4 ng .. 4 ng + 3; in elementwise work,
-// the channel pair's step ng of a slice.
+// the channel pair's steps ng, ng + kG, ... of a slice.
 struct Cell {
     int warp, lane, cg, ng, c;
     bool valid;  // the channels exist (they come in pairs: D is a multiple of 4)
@@ -253,8 +255,8 @@ __device__ __forceinline__ Cell cell_of(const Unit& un)
     Cell x;
     x.lane = threadIdx.x & 31;
     x.warp = threadIdx.x >> 5;
-    x.cg = x.lane >> 2;
-    x.ng = x.lane & 3;
+    x.cg = x.lane / kG;
+    x.ng = x.lane % kG;
     x.c = x.warp * kWC + 2 * x.cg;
     x.valid = x.c < un.cv;
     return x;
@@ -330,7 +332,7 @@ __device__ __forceinline__ void prepass(const BwdParams& p, const Unit& un, cons
     const int rows = min(un.t1 - t, kTL);
     const float2 bias = again2(&sm.cta.bias[x.c]);
 #pragma unroll
-    for (int r = x.ng; r < kTL; r += kT) {
+    for (int r = x.ng; r < kTL; r += kG) {
         float2 dl = dup(0.f), w = dl, dy = dl;
         if (r < rows && x.valid) {
             dl = __fadd2_rn(pair_at(&st.delta[r][x.c]), bias);
@@ -353,8 +355,10 @@ __device__ __forceinline__ void prepass(const BwdParams& p, const Unit& un, cons
 #pragma unroll
     for (int i = 0; i < kBC; ++i) {
         const int j = threadIdx.x + i * kBwdThreads;
-        sm.B[j / kNP][j % kNP] = ld1(&bc[i][0]);
-        sm.C[j / kNP][j % kNP] = ld1(&bc[i][1]);
+        if (j < kTL * kNP) {
+            sm.B[j / kNP][j % kNP] = ld1(&bc[i][0]);
+            sm.C[j / kNP][j % kNP] = ld1(&bc[i][1]);
+        }
     }
 }
 
@@ -476,17 +480,25 @@ __device__ __forceinline__ void finish_slice(const BwdParams& p, const Unit& un,
     using P2 = Pair<io_t>;
     using raw = typename P2::raw;
     constexpr bool PRECISE = std::is_same<io_t, float>::value;
-    const int r = r0 + x.ng;
-    if (t + x.ng < un.t1 && x.valid) {
+#pragma unroll
+    for (int step = x.ng; step < kT; step += kG) {
+        const int r = r0 + step;
+        if (t + step >= un.t1 || !x.valid)
+            continue;
         const float2 dl = sm.scal[x.warp][r][0][x.cg], dy = sm.scal[x.warp][r][2][x.cg];
         const float2 u = pair_at(&st.u[r][x.c]);
         auto sum = [&](int q) {
-            const float* s = &sm.part[x.warp][q][x.ng][2 * x.cg];
-            const float2 a = *reinterpret_cast<const float2*>(s);
-            const float2 b = *reinterpret_cast<const float2*>(s + kWC);
-            const float2 c = *reinterpret_cast<const float2*>(s + 2 * kWC);
-            const float2 d = *reinterpret_cast<const float2*>(s + 3 * kWC);
-            return __fadd2_rn(__fadd2_rn(a, b), __fadd2_rn(c, d));
+            const float* s = &sm.part[x.warp][q][step][2 * x.cg];
+            float2 v[kG];
+#pragma unroll
+            for (int g = 0; g < kG; ++g)
+                v[g] = *reinterpret_cast<const float2*>(s + g * kWC);
+#pragma unroll
+            for (int m = 1; m < kG; m *= 2)
+#pragma unroll
+                for (int g = 0; g < kG; g += 2 * m)
+                    v[g] = __fadd2_rn(v[g], v[g + m]);
+            return v[0];
         };
         const float2 gB = sum(1);
         float2 gA = sum(2);
@@ -500,14 +512,14 @@ __device__ __forceinline__ void finish_slice(const BwdParams& p, const Unit& un,
                                                   again2(&sm.cta.bias[x.c]))));
         dskip = __ffma2_rn(dy, u, dskip);
         dbias = __fadd2_rn(dbias, dd);
-        const uint32_t at = un.row(t + x.ng) + x.c;
+        const uint32_t at = un.row(t + step) + x.c;
         void* out = again(sm.cta.du);
         if (p.du_part)
             *reinterpret_cast<float2*>(static_cast<float*>(out) + at) = du;
         else
             *reinterpret_cast<raw*>(static_cast<io_t*>(out) + at) = P2::r(du);
         *reinterpret_cast<raw*>(static_cast<io_t*>(again(sm.cta.ddelta)) +
-                                (static_cast<uint32_t>(t + x.ng) * un.D + x.c)) = P2::r(dd);
+                                (static_cast<uint32_t>(t + step) * un.D + x.c)) = P2::r(dd);
         if (p.z) {
             const float2 z = pair_at(&st.z[r][x.c]), sg = sigmoid_2(z);
             const float2 y = __ffma2_rn(skip, u, sum(0));
@@ -522,20 +534,28 @@ __device__ __forceinline__ void finish_slice(const BwdParams& p, const Unit& un,
                 *reinterpret_cast<raw*>(static_cast<io_t*>(out) + at) = P2::r(dz);
         }
     }
-    // a lane adds the 8 channel pairs of one (step, tensor, 4 states); the lanes of the two
-    // tensors start one row apart, so that their banks differ
-    const int n4 = x.lane & 3, q = (x.lane >> 2) & 1, step = x.lane >> 3;
+    // kP lanes add 8 channel pairs each of one (step, tensor, 4 states); lanes of different tensors
+    // and parts start at different rows, so that their banks differ
+    constexpr int kP = 4 / kG;
+    const int n4 = x.lane % kG, q = x.lane / kG & 1, part = x.lane / (2 * kG) % kP, step = x.lane >> 3;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < kWC / 2; ++i) {
+    for (int i = 0; i < 8; ++i) {
         const float4 w = *reinterpret_cast<const float4*>(
-            &sm.dbc[x.warp][step][q][(i + q) & (kWC / 2 - 1)][4 * n4]);
+            &sm.dbc[x.warp][step][q][8 * part + ((i + 2 * part + q) & 7)][4 * n4]);
         v.x += w.x;
         v.y += w.y;
         v.z += w.z;
         v.w += w.w;
     }
-    sm.acc[r0 + step][q][x.warp][n4] = v;
+    if (kP > 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, 4);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, 4);
+        v.z += __shfl_xor_sync(0xffffffffu, v.z, 4);
+        v.w += __shfl_xor_sync(0xffffffffu, v.w, 4);
+    }
+    if (part == 0)
+        sm.acc[r0 + step][q][x.warp][n4] = v;
 }
 
 // dB and dC of a finished tile: the sums of the four warps, to the CTA's partial sums.
@@ -723,7 +743,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
         }
     }
 #pragma unroll
-    for (int m = 1; m < 4; m *= 2) {
+    for (int m = 1; m < kG; m *= 2) {
         dskip.x += __shfl_xor_sync(0xffffffffu, dskip.x, m);
         dskip.y += __shfl_xor_sync(0xffffffffu, dskip.y, m);
         dbias.x += __shfl_xor_sync(0xffffffffu, dbias.x, m);
