@@ -42,8 +42,8 @@
  *     memory has been read or written.  SS_ERR_CUDA means the runtime failed; when it failed
  *     at a later launch of a call (the scan after the segment aggregates, or the direction
  *     merge), the earlier launches of that call have been enqueued.
- *   - `stream` must belong to the current device (SS_ERR_DEVICE otherwise): the library's
- *     device-side words are looked up on the current device.
+ *   - `stream` must belong to the current device (SS_ERR_DEVICE otherwise; not checked while the
+ *     stream is captured): the library's device-side words are looked up on the current device.
  *   - Base pointers of u, delta, B, C, z, out and workspace must be 16-byte aligned, and
  *     dim * sizeof(io element) must be a multiple of 16 (SS_ERR_ALIGN otherwise).
  *   - N (dstate) is at most SS_MAX_DSTATE; at most SS_MAX_DIRS directions.

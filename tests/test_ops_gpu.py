@@ -152,7 +152,8 @@ def test_recurrence_step_by_step_is_the_sequence(cuda_device):
 def test_recurrence_gradient_against_differences(cuda_device):
     # <gradient, v> against (f(x + e v) - f(x - e v)) / 2e of the plain 64-bit forward pass; the
     # difference quotient of the smooth f is off by e^2 f''' / 6 and by rounding, both far below
-    # the bound
+    # the bound.  The bound: an element of the gradient is off by at most 5e-5 (|g| + rms), so with
+    # independent normal v the sum is off by about 1e-4 |gradient|, times a few standard deviations
     t = rec_inputs(10, 2, 90, 16, F32, "sigmoid")
     names = ("x", "gate", "gate_bias", "initial_state")
     xs = dict(zip(names, cuda(*(t[n] for n in names))))
@@ -799,6 +800,50 @@ def test_outputs_stay_in_their_bounds(cuda_device, io):
             ops.selective_state_load(*args, o["back%d" % bits][0], bits=bits)
         torch.cuda.synchronize()
         check_guards(o, ("out", "state", "cs", "scales8", "back8", "scales4", "back4"))
+
+
+def test_far_rows_and_slots(cuda_device):
+    # element offsets beyond 2^31: what lies there equals the same rows and slots in small tensors
+    g = torch.Generator(device="cuda").manual_seed(230)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda", dtype=BF16)  # noqa: E731
+    b, L, D = 3, 131072, 6144
+    assert (b - 1) * L * D > 2 ** 30 and b * L * D > 2 ** 31
+    x, gate = rand(b, L, D), rand(b, L, D)
+    gb = torch.full((D,), 3.0, device="cuda")
+    out, last = ops.gated_recurrence_fwd(x, gate, gate_bias=gb, complement=True,
+                                         return_last_state=True)
+    x, gate = x[2:].clone(), gate[2:].clone()
+    o, la = ops.gated_recurrence_fwd(x, gate, gate_bias=gb, complement=True, return_last_state=True)
+    ref.close(out[2, -100:], o[0, -100:], tol=2.0 ** -7)  # (two roundings: the cluster may differ)
+    ref.close(last[2], la[0])
+    del x, gate, out, o
+    torch.cuda.empty_cache()
+    slots, D, N = 28000, 5120, 16
+    assert slots * D * N > 2 ** 31
+    s = step_inputs(231, 2, D, N, BF16, width=4, slots=2)
+    f = dict(zip(s, cuda(*s.values())))
+    far = torch.tensor([slots - 1, 7], dtype=torch.int32, device="cuda")
+    pool = torch.empty(slots, D, N, device="cuda")
+    window = torch.empty(slots, 3, D, dtype=BF16, device="cuda")
+    pool[far.long()], window[far.long()] = f["state"], f["cs"]
+    args = (f["u"], f["delta"], f["A"], f["B"], f["C"])
+    kw = dict(D=f["D"], z=f["z"], delta_bias=f["bias"], conv_weight=f["cw"], conv_bias=f["cb"])
+    out = ops.selective_scan_step(*args, pool, slots=far, conv_state=window, **kw)
+    near = ops.selective_scan_step(*args, f["state"], conv_state=f["cs"], **kw)
+    assert torch.equal(out, near) and torch.equal(pool[far.long()], f["state"])
+    assert torch.equal(window[far.long()], f["cs"])
+    for bits in (8, 4):
+        codes = torch.empty(slots, D, N * bits // 8, dtype=torch.int8, device="cuda")
+        scales = torch.empty(slots, D, device="cuda")
+        c2, s2 = (torch.empty(2, *v.shape[1:], dtype=v.dtype, device="cuda") for v in (codes, scales))
+        ops.selective_state_store(pool, codes, scales, bits=bits, src_slots=far, dst_slots=far)
+        ops.selective_state_store(f["state"], c2, s2, bits=bits)
+        assert torch.equal(codes[far.long()], c2) and torch.equal(scales[far.long()], s2)
+        back = f["state"].clone()
+        ops.selective_state_load(codes, scales, pool, bits=bits, src_slots=far, dst_slots=far)
+        ops.selective_state_load(c2, s2, back, bits=bits)
+        assert torch.equal(pool[far.long()], back)
+        pool[far.long()] = f["state"]
 
 
 def test_forward_scan_and_training_step_captured(cuda_device):
