@@ -846,6 +846,27 @@ def test_far_rows_and_slots(cuda_device):
         pool[far.long()] = f["state"]
 
 
+def test_scan_bwd_far_rows(cuda_device):
+    # a batch of more than 2^31 elements: its last row's gradients equal the row's own (the segments
+    # of the two calls may differ, so two roundings to bf16 lie between them)
+    g = torch.Generator(device="cuda").manual_seed(240)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda", dtype=BF16)  # noqa: E731
+    b, L, D, N = 3, 131072, 6144, 4
+    assert b * L * D > 2 ** 31
+    dout, u, delta, z = (rand(b, L, D) for _ in range(4))
+    B, C = rand(b, L, N), rand(b, L, N)
+    A = -torch.rand(D, N, generator=g, device="cuda") - 0.5
+    o = ops.selective_scan_bwd(dout, u, delta, A, B, C, z=z)
+    far = {k: o[k][2:, -64:].clone() for k in ("du", "ddelta", "dz")}
+    far |= {k: o[k].reshape(b, L, N)[2:, -64:].clone() for k in ("dB", "dC")}
+    del o
+    dout, u, delta, z, B, C = (v[2:].clone() for v in (dout, u, delta, z, B, C))
+    torch.cuda.empty_cache()
+    o = ops.selective_scan_bwd(dout, u, delta, A, B, C, z=z)
+    for k, v in far.items():
+        ref.close(v, o[k].reshape(1, L, -1)[:, -64:], tol=2.0 ** -7)
+
+
 def test_forward_scan_and_training_step_captured(cuda_device):
     # the forward scan under capture, alone and with its gradient as a whole training step
     t = scan_inputs(194, 2, 200, 40, 16, BF16, dirs=(0, 1))
