@@ -6,6 +6,12 @@ they check shapes, dtypes and devices, allocate outputs and workspaces that the 
 (from PyTorch's allocator, on the current stream) and call the library on the current CUDA stream
 of the tensors' device, which has to be the current device.  selective_scan and gated_recurrence
 wrap forward and gradient for torch.autograd.  There is no CPU path.
+
+A training step through those two can be captured into a CUDA graph after one eager step.  Nothing
+of an eager graph of the same leaves (an output or loss of theirs) may then be alive: PyTorch keeps
+a leaf's accumulation node, and with it the eager stream, for as long as such a graph lives, a
+captured backward pass would wait for that uncaptured stream, and PyTorch ends the process.  Delete
+the eager outputs first, or capture with detached leaves of the same storage.
 """
 
 from __future__ import annotations
