@@ -15,12 +15,18 @@
 // segments after all: a first launch (`aggregate`) only composes each segment's map, the second
 // starts every segment from the maps before it.
 //
-// a - 1 is what is kept, not a: next to a decay of one, a rounded to fp32 loses 2^-25 of the state
-// at every step, and 1 - a keeps its relative accuracy.
+// A step is a h + w, with a itself: a gate that closes leaves nothing of the old state but a h, and an
+// infinite state stays infinite.  Next to a decay of one that would lose 2^-25 of the state (and the
+// exponential's error) at every step, which a memory of 1000 steps multiplies.  It does not come to
+// that, because states go from one warp's steps to the next through the products P alone: a product
+// gets back what its factors lost, by 1 - a, which is known to its own accuracy (sigmoid: P (1 + sum of
+// (1 - a) - what 1 - a is); exp: the exponential of the sum).
 //
 // Measured on B200 (8 x 2048 x 1536 bf16): CTAs of 4 warps, 16 steps a warp, 36.9 us; of 8 warps 41
 // us; of 16 warps with 8 steps 47 us (the barriers cost more than the shorter chains give).  More
 // than about three CTAs on an SM run slower, not faster.  TMA boxes for the rows: the same times.
+// a - 1 alone, which is wrong where gates close, took 33.0 us among other passes where this takes 35.2
+// (1 x 131072 x 5120: 729 and 785); a = k + m with k = 0 or 1 for every step, as right as this, 39.0 (862).
 #pragma once
 
 #include <type_traits>
@@ -52,24 +58,54 @@ template <typename io_t, bool BWD> struct RecSmem {
     uint64_t maps[2];  // the maps of the cluster's CTAs have landed
 };
 
-// a - 1 of two gates.  `bias2` is the bias times log2(e): the sums are taken in base 2, where the
-// exponential is one instruction.  The sigmoid's 1 - a is sigmoid(-s), accurate in both tails; s =
-// -inf gives exp 0 and a - 1 = -1.
-template <int FORM, bool ACCURATE>
-__device__ __forceinline__ float2 decay_minus_one(float2 gate, float2 bias2)
+// A decay, and a product of decays, is at least 2^-149 (of a gate of -inf too): that takes a finite
+// state below the normal range, and does not make NaN of an infinite one.
+constexpr float kLeast = 0x1p-149f;
+// The sigmoid's logarithm is at least -125, where 1 + exp(-s) and its reciprocal are normal numbers; what
+// is left of the decay there is taken off again (of all: 2^-25 of a decay of 2^-100, less above).
+constexpr float kLeastLog2 = -125.f, kLeft = 0x1p-125f - 0x1p-145f;
+
+__device__ __forceinline__ float2 at_least(float2 v, float least)  // (of P: NaN has its say in H)
 {
-    const float2 log2e = make_float2(kLog2e, kLog2e), minus = make_float2(-1.f, -1.f);
-    const float2 shift = make_float2(kDecayShift, kDecayShift);
-    const float2 s = __ffma2_rn(gate, log2e, FORM == SS_GATE_SIGMOID ? bias2 : shift);
-    const float2 e = make_float2(ex2(s.x), ex2(s.y));
+    return make_float2(fmaxf(v.x, least), fmaxf(v.y, least));
+}
+
+// The same, and NaN stays.
+__device__ __forceinline__ float at_least_nan(float v, float least)
+{
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(v), "f"(least));
+    return m;
+}
+
+// The decays a of two gates and 1 - a, both relatively accurate.  `bias2` is the bias times log2(e): the
+// sums are taken in base 2, where the exponential is one instruction.  The exp form leaves 1 - a out
+// without REST.
+template <int FORM, bool REST>
+__device__ __forceinline__ void decays_of(float2 gate, float2 bias2, float2& a, float2& rest)
+{
+    const float2 log2e = make_float2(kLog2e, kLog2e), one = make_float2(1.f, 1.f);
     if (FORM == SS_GATE_SIGMOID) {
-        const float2 q = __ffma2_rn(e, minus, minus);
-        return make_float2(rcp(q.x), rcp(q.y));
+        const float2 s = __ffma2_rn(gate, log2e, bias2);
+        const float2 e = make_float2(ex2(-at_least_nan(s.x, kLeastLog2)),
+                                     ex2(-at_least_nan(s.y, kLeastLog2)));
+        const float2 q = __fadd2_rn(e, one);
+        a = make_float2(rcp(q.x), rcp(q.y));
+        rest = __fmul2_rn(e, a);
+        a = __fadd2_rn(a, make_float2(-kLeft, -kLeft));
+    } else {
+        const float2 s = __fmul2_rn(gate, log2e);
+        a = make_float2(at_least_nan(ex2(s.x), kLeast), at_least_nan(ex2(s.y), kLeast));
+        if (REST)
+            rest = make_float2(one_minus_exp(gate.x, a.x), one_minus_exp(gate.y, a.y));
     }
-    // without the polynomial the error is that of ex2, 2^-22 of the state a step
-    if (ACCURATE)
-        return make_float2(-one_minus_exp(gate.x, e.x), -one_minus_exp(gate.y, e.y));
-    return __fadd2_rn(e, minus);
+}
+
+// exp(x), next to one to half a step.
+__device__ __forceinline__ float exp_of(float x)
+{
+    const float e = ex2(x * kLog2e);
+    return fabsf(x) <= 0.35f ? 1.f - one_minus_exp(x, e) : e;
 }
 
 // 16 bytes global -> shared, zeros where !valid.
@@ -122,21 +158,20 @@ __device__ __forceinline__ float2 through(float4 m, float2 h)
 // The map f after the map m.
 __device__ __forceinline__ float4 compose(float4 f, float4 m)
 {
-    const float2 P = __fmul2_rn(make_float2(f.x, f.y), make_float2(m.x, m.y));
+    const float2 P = at_least(__fmul2_rn(make_float2(f.x, f.y), make_float2(m.x, m.y)), kLeast);
     const float2 H = through(f, make_float2(m.z, m.w));
     return make_float4(P.x, P.y, H.x, H.y);
 }
 
 // BACK: step s of the recurrence (in the order it runs) lies at position L-1-s.
 template <typename io_t, int FORM, bool COMP, bool BWD, bool BACK>
-__global__ void __launch_bounds__(kRecThreads, 4)
+__global__ void __launch_bounds__(kRecThreads, 3)
     recurrence_kernel(const __grid_constant__ RecParams p)
 {
     using T = RecTile<io_t, BWD>;
     using P2 = Pair<io_t>;
     using raw = typename P2::raw;
     constexpr int N = T::kSteps;
-    constexpr bool ACCURATE = COMP || std::is_same<io_t, float>::value;
     extern __shared__ __align__(128) unsigned char raw_smem[];
     RecSmem<io_t, BWD>& sm = *reinterpret_cast<RecSmem<io_t, BWD>*>(raw_smem);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -220,8 +255,8 @@ __global__ void __launch_bounds__(kRecThreads, 4)
         }
     }
     bool waits = true;  // false once a wait has given up: the rest runs without waiting
-    const float2 minus = make_float2(-1.f, -1.f);
-    float2 db = make_float2(0.f, 0.f);  // -dbias
+    const float2 minus = make_float2(-1.f, -1.f), one = make_float2(1.f, 1.f);
+    float2 db = make_float2(0.f, 0.f);  // dbias
     for (int m = 0; m < rounds; ++m) {
         const int st = m & 1;
         const int s0 = t0 + (m * cs + rank) * T::kRows + warp * N;  // this warp's first step
@@ -236,30 +271,51 @@ __global__ void __launch_bounds__(kRecThreads, 4)
         auto at = [&](int q, int i) {
             return *reinterpret_cast<const raw*>(mine + (q * T::kRows + i) * kRecCh);
         };
-        float2 c[N];
-        raw v[N];  // x, or dout
-        float2 P = make_float2(1.f, 1.f), H = make_float2(0.f, 0.f);
+        float2 a[N];
+        float2 rest[BWD ? N : 1];  // 1 - a
+        // what comes in: x, (1 - a) x or dout
+        constexpr bool SCALED = COMP && !BWD;
+        typename std::conditional<SCALED, float2, raw>::type v[N];
+        auto in = [&](int i) {
+            if constexpr (SCALED)
+                return v[i];
+            else
+                return P2::f(v[i]);
+        };
+        float2 P = one, H = make_float2(0.f, 0.f);
+        float2 lost = make_float2(0.f, 0.f);  // exp: the sum of the gates
         // steps behind the end keep the state
         auto compose_steps = [&](bool whole) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                v[i] = at(1, i);
-                c[i] = decay_minus_one<FORM, ACCURATE>(P2::f(at(0, i)), bias);
-                if (!whole && s0 + i >= t1) {
-                    c[i] = make_float2(0.f, 0.f);
-                    v[i] = raw{};
+                const float2 gate = P2::f(at(0, i));
+                float2& r = rest[BWD ? i : 0];
+                decays_of<FORM, COMP>(gate, bias, a[i], r);
+                if constexpr (SCALED)
+                    v[i] = __fmul2_rn(r, P2::f(at(1, i)));
+                else
+                    v[i] = at(1, i);
+                const bool inside = whole || s0 + i < t1;
+                if (!inside) {
+                    a[i] = one;
+                    v[i] = {};
                 }
-                const float2 w = P2::f(v[i]);
-                if (BWD) {
-                    H = __fadd2_rn(H, w);
-                    H = __ffma2_rn(c[i], H, H);
-                } else if (COMP) {
-                    H = __ffma2_rn(c[i], __ffma2_rn(w, minus, H), H);
-                } else {
-                    H = __fadd2_rn(__ffma2_rn(c[i], H, w), H);
-                }
-                P = __ffma2_rn(c[i], P, P);
+                if (inside && FORM == SS_GATE_EXP)
+                    lost = __fadd2_rn(lost, gate);
+                else if (inside)
+                    lost = __fadd2_rn(lost, __ffma2_rn(r, minus, __ffma2_rn(a[i], minus, one)));
+                if (BWD)
+                    H = __fmul2_rn(a[i], __fadd2_rn(H, in(i)));
+                else
+                    H = __ffma2_rn(a[i], H, in(i));
+                if (FORM == SS_GATE_SIGMOID)
+                    P = __fmul2_rn(a[i], P);
             }
+            if (FORM == SS_GATE_SIGMOID)
+                P = __ffma2_rn(P, lost, P);
+            else
+                P = make_float2(exp_of(lost.x), exp_of(lost.y));
+            P = at_least(P, kLeast);
         };
         const bool whole = s0 + N <= t1;
         if (whole)
@@ -304,11 +360,11 @@ __global__ void __launch_bounds__(kRecThreads, 4)
                         if (q == rank)
                             h = carry;
                         carry = through(f, carry);
-                        product = __fmul2_rn(product, make_float2(f.x, f.y));
+                        product = at_least(__fmul2_rn(product, make_float2(f.x, f.y)), kLeast);
                     }
             } else {
                 carry = through(all, carry);
-                product = __fmul2_rn(product, make_float2(all.x, all.y));
+                product = at_least(__fmul2_rn(product, make_float2(all.x, all.y)), kLeast);
             }
             sm.start[lane] = h;
         }
@@ -324,32 +380,27 @@ __global__ void __launch_bounds__(kRecThreads, 4)
         auto run_steps = [&](bool whole) {
 #pragma unroll
             for (int i = 0; i < N; ++i, out += stride, dgate += BWD ? stride : 0) {
-                const float2 w = P2::f(v[i]);
                 const bool real = active && (whole || s0 + i < t1);
                 if (BWD) {
-                    const float2 G = __fadd2_rn(h, w);
-                    h = __ffma2_rn(c[i], G, G);
+                    const float2 G = __fadd2_rn(h, in(i));
+                    h = __fmul2_rn(a[i], G);
                     float2 before = P2::f(at(2, i));
                     if (s0 + i == L - 1)
                         before = p.init && active
                                      ? make_float2(p.init[b * p.D + d], p.init[b * p.D + d + 1])
                                      : make_float2(0.f, 0.f);
-                    // -ds, for every form
                     if (COMP)
                         before = __ffma2_rn(P2::f(at(T::kTensors - 1, i)), minus, before);
                     float2 ds = __fmul2_rn(h, before);
-                    ds = FORM == SS_GATE_SIGMOID ? __fmul2_rn(ds, c[i]) : __fmul2_rn(ds, minus);
+                    if (FORM == SS_GATE_SIGMOID)
+                        ds = __fmul2_rn(ds, rest[i]);
                     if (real) {
                         db = __fadd2_rn(db, ds);
-                        const float2 dx = COMP ? __fmul2_rn(c[i], G) : __fmul2_rn(G, minus);
-                        *reinterpret_cast<raw*>(out) = P2::r(make_float2(-dx.x, -dx.y));
-                        *reinterpret_cast<raw*>(dgate) = P2::r(make_float2(-ds.x, -ds.y));
+                        *reinterpret_cast<raw*>(out) = P2::r(COMP ? __fmul2_rn(rest[i], G) : G);
+                        *reinterpret_cast<raw*>(dgate) = P2::r(ds);
                     }
                 } else {
-                    if (COMP)
-                        h = __ffma2_rn(c[i], __ffma2_rn(w, minus, h), h);
-                    else
-                        h = __fadd2_rn(__ffma2_rn(c[i], h, w), h);
+                    h = __ffma2_rn(a[i], h, in(i));
                     if (real)
                         *reinterpret_cast<raw*>(out) = P2::r(h);
                 }
@@ -377,7 +428,7 @@ __global__ void __launch_bounds__(kRecThreads, 4)
             for (int w = 1; w < kRecWarps; ++w)
                 db = __fadd2_rn(db, part[w * 32 + lane]);
             *reinterpret_cast<float2*>(p.dbias_part + ((static_cast<int64_t>(b) * p.S + seg) * cs + rank) * p.D + d) =
-                make_float2(-db.x, -db.y);
+                db;
         }
     }
     ss::pdl_launch_dependents();
