@@ -25,8 +25,8 @@
 // Measured on B200 (8 x 2048 x 1536 bf16): CTAs of 4 warps, 16 steps a warp, 36.9 us; of 8 warps 41
 // us; of 16 warps with 8 steps 47 us (the barriers cost more than the shorter chains give).  More
 // than about three CTAs on an SM run slower, not faster.  TMA boxes for the rows: the same times.
-// a - 1 alone, which is wrong where gates close, took 33.0 us among other passes where this takes 35.2
-// (1 x 131072 x 5120: 729 and 785); a = k + m with k = 0 or 1 for every step, as right as this, 39.0 (862).
+// a - 1 alone, which is wrong where gates close, took 33.0 us among other passes where this takes 36.0
+// (1 x 131072 x 5120: 730 and 786); a = k + m with k = 0 or 1 for every step, as right as this, 39.0 (862).
 #pragma once
 
 #include <type_traits>
@@ -78,15 +78,15 @@ __device__ __forceinline__ float at_least_nan(float v, float least)
     return m;
 }
 
-// The decays a of two gates and 1 - a, both relatively accurate.  `bias2` is the bias times log2(e): the
-// sums are taken in base 2, where the exponential is one instruction.  The exp form leaves 1 - a out
-// without REST.
+// The decays a of two gates and 1 - a, both relatively accurate.  Gate and bias are added before the
+// product with log2(e), whose rounding would otherwise be that of the larger one: where 1001 and -1000
+// meet, 4e-5 of 1 - a.  The exp form leaves 1 - a out without REST.
 template <int FORM, bool REST>
-__device__ __forceinline__ void decays_of(float2 gate, float2 bias2, float2& a, float2& rest)
+__device__ __forceinline__ void decays_of(float2 gate, float2 bias, float2& a, float2& rest)
 {
     const float2 log2e = make_float2(kLog2e, kLog2e), one = make_float2(1.f, 1.f);
     if (FORM == SS_GATE_SIGMOID) {
-        const float2 s = __ffma2_rn(gate, log2e, bias2);
+        const float2 s = __fmul2_rn(__fadd2_rn(gate, bias), log2e);
         const float2 e = make_float2(ex2(-at_least_nan(s.x, kLeastLog2)),
                                      ex2(-at_least_nan(s.y, kLeastLog2)));
         const float2 q = __fadd2_rn(e, one);
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kRecThreads, 3)
     const int64_t base = static_cast<int64_t>(b) * p.L * p.D + d;
     float2 bias = make_float2(0.f, 0.f);
     if (p.bias && active)
-        bias = make_float2(p.bias[d] * kLog2e, p.bias[d + 1] * kLog2e);
+        bias = make_float2(p.bias[d], p.bias[d + 1]);
     const float* first = BWD ? p.dlast : p.init;
     float2 carry = make_float2(0.f, 0.f);  // the state before this round (kept by warp 0)
     if (first && active)

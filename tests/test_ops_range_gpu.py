@@ -149,6 +149,26 @@ def test_states_next_to_overflow(cuda_device, complement):
     each(out[:, :want.shape[1]], want, 5e-6, "out")
 
 
+# ----------------------------------------------------------------------------- gates and biases
+
+def test_gates_and_biases_that_cancel(cuda_device):
+    # gate + bias is exact in fp32 (multiples of 2^-10 below 2^12), so 1 - a has the accuracy that
+    # it has for the sum itself
+    g = gen(4)
+    b, L, D = 2, 70, 40
+    bias = 1000 + torch.randint(0, 1024, (D,), generator=g) / 1024
+    gate = -998 + torch.randint(-2048, 2048, (b, L, D), generator=g) / 1024
+    out, dout, x = positive(g, b, L, D), positive(g, b, L, D), -positive(g, b, L, D)
+    got = ops.gated_recurrence_bwd(dout.cuda(), x.cuda(), gate.cuda(), out.cuda(),
+                                   gate_bias=bias.cuda(), complement=True)
+    want = ref.recurrence_grads(ref.f64(dout), ref.f64(x), ref.f64(gate), ref.f64(out),
+                                ref.f64(bias), complement=True)
+    # a step's gradient gathers the errors of at most some 1/(1 - a) < 150 decays a to come, each
+    # 2^-22 (1 - a) on top of three roundings of both signs: below 3e-6
+    for name, a, w in zip(("dx", "dgate", "dbias"), got, want):
+        each(a, w, 6e-6, name)
+
+
 # ----------------------------------------------------------------------------- long memories
 
 @pytest.mark.parametrize("io", [F32, BF16])
