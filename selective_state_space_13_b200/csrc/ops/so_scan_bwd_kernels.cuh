@@ -25,8 +25,9 @@
 // dB, dC and the parameter gradients leave each CTA as fp32 partial sums that a last launch adds
 // in a fixed order.
 //
-// fp32 io takes the decays as Abar - 1 = expm1(Delta A) and updates h <- h + ((Abar - 1) h + w B):
-// a decay near one, rounded to fp32, would lose 2^-25 of the state every step.
+// A decay near one, rounded to fp32, and the error of its exponential lose up to 2^-22 of the state every
+// step, which a long memory multiplies.  fp32 io gets that back once a slice: the product of the slice's
+// decays, as they are, against exp(A sum Delta) - 1, which is relatively accurate (Slice).
 #pragma once
 
 #include <type_traits>
@@ -72,12 +73,6 @@ __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;
 __device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
 
 __device__ __forceinline__ float2 ex2_2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
-
-// exp(x) - 1, relative error about 1e-7.
-__device__ __forceinline__ float2 expm1_2(float2 x)
-{
-    return make_float2(-one_minus_exp(x.x, ex2(x.x * kLog2e)), -one_minus_exp(x.y, ex2(x.y * kLog2e)));
-}
 
 // What a CTA works on.  Element offsets inside one sequence fit in 32 bits (L * D < 2^31).
 struct Unit {
@@ -262,9 +257,7 @@ __device__ __forceinline__ Cell cell_of(const Unit& un)
     return x;
 }
 
-// A of the thread's cells, times log2(e) for the exponentials in base 2 (not for fp32 io, which
-// takes expm1).
-template <bool PRECISE>
+// A of the thread's cells, times log2(e) for the exponentials in base 2.
 __device__ __forceinline__ void load_A(const BwdParams& p, const Unit& un, const Cell& x, float2 A[4])
 {
     const int64_t d = (p.params_per_dir ? un.k * p.D : 0) + un.c0 + x.c;
@@ -274,27 +267,54 @@ __device__ __forceinline__ void load_A(const BwdParams& p, const Unit& un, const
         A[i] = dup(0.f);
         if (x.valid && n < p.N)
             A[i] = make_float2(p.A[d * p.N + n], p.A[(d + 1) * p.N + n]);
-        if (!PRECISE)
-            A[i] = __fmul2_rn(A[i], dup(kLog2e));
+        A[i] = __fmul2_rn(A[i], dup(kLog2e));
     }
 }
 
-// The decay of a step: Abar, or Abar - 1 with PRECISE.
+// The decay of a step.
 template <bool PRECISE> __device__ __forceinline__ float2 decay(float2 delta, float2 A)
 {
-    return PRECISE ? expm1_2(__fmul2_rn(delta, A)) : ex2_2(__ffma2_rn(delta, A, dup(kDecayShift)));
+    return ex2_2(PRECISE ? __fmul2_rn(delta, A) : __ffma2_rn(delta, A, dup(kDecayShift)));
 }
 
-// Abar v + w with that decay.
-template <bool PRECISE> __device__ __forceinline__ float2 decayed(float2 a, float2 v, float2 w)
-{
-    return PRECISE ? __fadd2_rn(v, __ffma2_rn(a, v, w)) : __ffma2_rn(a, v, w);
-}
+// What the decays of a slice have lost (PRECISE).
+struct Slice {
+    float2 sum, size;  // of Delta, of its magnitude
+    float2 Q[4];       // the product of the decays, minus one
 
-template <bool PRECISE> __device__ __forceinline__ float2 decayed(float2 a, float2 v)
-{
-    return PRECISE ? __ffma2_rn(a, v, v) : __fmul2_rn(a, v);
-}
+    __device__ __forceinline__ void start()
+    {
+        sum = size = Q[0] = Q[1] = Q[2] = Q[3] = dup(0.f);
+    }
+    __device__ __forceinline__ void step(float2 delta)
+    {
+        sum = __fadd2_rn(sum, delta);
+        size = make_float2(size.x + fabsf(delta.x), size.y + fabsf(delta.y));
+    }
+    __device__ __forceinline__ void decayed_by(int i, float2 a)
+    {
+        const float2 c = __fadd2_rn(a, dup(-1.f));
+        Q[i] = __ffma2_rn(Q[i], c, __fadd2_rn(Q[i], c));
+    }
+    // v with it: decays that are not near one do not come to much in the few steps that they are
+    // remembered.
+    __device__ __forceinline__ float2 restored(int i, float2 A, float2 v) const
+    {
+        // 2^x - 1 = x ln 2 (1 + x ln 2 / 2 (1 + ...)), to x^8 (below 1e-9 relative for |x| <= 1/2)
+        const float2 x = __fmul2_rn(sum, A), most = __fmul2_rn(size, A);
+        const float2 y = __fmul2_rn(x, dup(kLn2));
+        float2 e = __ffma2_rn(y, dup(1.f / 40320.f), dup(1.f / 5040.f));
+        e = __ffma2_rn(e, y, dup(1.f / 720.f));
+        e = __ffma2_rn(e, y, dup(1.f / 120.f));
+        e = __ffma2_rn(e, y, dup(1.f / 24.f));
+        e = __ffma2_rn(e, y, dup(1.f / 6.f));
+        e = __ffma2_rn(e, y, dup(0.5f));
+        e = __ffma2_rn(e, y, dup(1.f));
+        const float2 lost = __ffma2_rn(e, y, __fmul2_rn(Q[i], dup(-1.f)));
+        return __ffma2_rn(v, make_float2(fabsf(most.x) <= 0.5f ? lost.x : 0.f,
+                                         fabsf(most.y) <= 0.5f ? lost.y : 0.f), v);
+    }
+};
 
 template <typename io_t> __device__ __forceinline__ float2 pair_at(const io_t* p)
 {
@@ -418,12 +438,13 @@ __global__ void __launch_bounds__(kBwdThreads) summary_kernel(const __grid_const
     const Cell x = cell_of(un);
     fill_cta<io_t>(p, un, sm.cta);
     float2 A[4], h[4], P[4], G[4], cum = dup(0.f);
-    load_A<PRECISE>(p, un, x, A);
+    load_A(p, un, x, A);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         h[i] = G[i] = dup(0.f);
         P[i] = dup(1.f);
     }
+    Slice slice;
     io_t bc[kBC][2];
     issue<io_t>(p, un, sm.cta, un.t0, sm.st[0], SPLIT, bc);
     for (int t = un.t0, it = 0; t < un.t1; t += kTL, ++it) {
@@ -444,6 +465,11 @@ __global__ void __launch_bounds__(kBwdThreads) summary_kernel(const __grid_const
             load4(sm.B, r, x.ng, B);
             const float2 dl = sm.scal[x.warp][r][0][x.cg], w = sm.scal[x.warp][r][1][x.cg];
             float2 dy = dup(0.f);
+            if (PRECISE) {
+                if (r % kT == 0)
+                    slice.start();
+                slice.step(dl);
+            }
             if (SPLIT) {
                 load4(sm.C, r, x.ng, C);
                 dy = sm.scal[x.warp][r][2][x.cg];
@@ -452,10 +478,18 @@ __global__ void __launch_bounds__(kBwdThreads) summary_kernel(const __grid_const
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 a = decay<PRECISE>(dl, A[i]);
-                h[i] = decayed<PRECISE>(a, h[i], __fmul2_rn(w, B[i]));
+                h[i] = __ffma2_rn(a, h[i], __fmul2_rn(w, B[i]));
                 if (SPLIT) {
-                    P[i] = decayed<PRECISE>(a, P[i]);
+                    P[i] = __fmul2_rn(a, P[i]);
                     G[i] = __ffma2_rn(P[i], __fmul2_rn(dy, C[i]), G[i]);
+                }
+                if (PRECISE) {
+                    slice.decayed_by(i, a);
+                    if (r % kT == kT - 1) {
+                        h[i] = slice.restored(i, A[i], h[i]);
+                        if (SPLIT)
+                            P[i] = slice.restored(i, A[i], P[i]);
+                    }
                 }
             }
         }
@@ -479,7 +513,6 @@ __device__ __forceinline__ void finish_slice(const BwdParams& p, const Unit& un,
 {
     using P2 = Pair<io_t>;
     using raw = typename P2::raw;
-    constexpr bool PRECISE = std::is_same<io_t, float>::value;
 #pragma unroll
     for (int step = x.ng; step < kT; step += kG) {
         const int r = r0 + step;
@@ -501,9 +534,7 @@ __device__ __forceinline__ void finish_slice(const BwdParams& p, const Unit& un,
             return v[0];
         };
         const float2 gB = sum(1);
-        float2 gA = sum(2);
-        if (!PRECISE)
-            gA = __fmul2_rn(gA, dup(kLn2));  // A was in base 2
+        const float2 gA = __fmul2_rn(sum(2), dup(kLn2));  // A was in base 2
         const float2 skip = again2(&sm.cta.skip[x.c]);
         const float2 du = __ffma2_rn(skip, dy, __fmul2_rn(dl, gB));
         float2 dd = __ffma2_rn(u, gB, gA);
@@ -590,7 +621,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
     const Cell x = cell_of(un);
     fill_cta<io_t>(p, un, sm.cta);
     float2 A[4], g[4], dA[4];
-    load_A<PRECISE>(p, un, x, A);
+    load_A(p, un, x, A);
     float2 dskip = dup(0.f), dbias = dup(0.f);
 
     const int tiles = (un.t1 - un.t0 + kTL - 1) / kTL;
@@ -667,8 +698,7 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
                 get4(&sm.hstart[0][threadIdx.x], kBwdThreads, hstart);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    h[0][i] = __fadd2_rn(h[0][i], decayed<PRECISE>(decay<PRECISE>(next_cum, A[i]),
-                                                                   hstart[i]));
+                    h[0][i] = __ffma2_rn(decay<PRECISE>(next_cum, A[i]), hstart[i], h[0][i]);
             }
             if (t + r0 > un.t0) {
                 --slice;
@@ -685,10 +715,13 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     a[r][i] = decay<PRECISE>(dl, A[i]);
-                    h[r + 1][i] = decayed<PRECISE>(a[r][i], h[r][i], __fmul2_rn(w, B[i]));
+                    h[r + 1][i] = __ffma2_rn(a[r][i], h[r][i], __fmul2_rn(w, B[i]));
                 }
             }
             // the reverse recurrence
+            Slice slice;
+            if (PRECISE)
+                slice.start();
 #pragma unroll
             for (int r = kT - 1; r >= 0; --r) {
                 float2 B[4], C[4], y, gB, gA;
@@ -698,6 +731,8 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
                 const float2 w = sm.scal[x.warp][r0 + r][1][x.cg];
                 const float2 dy = sm.scal[x.warp][r0 + r][2][x.cg];
                 float dB[4], dC[4];
+                if (PRECISE)
+                    slice.step(dl);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     y = i ? __ffma2_rn(C[i], h[r + 1][i], y) : __fmul2_rn(C[i], h[r + 1][i]);
@@ -707,7 +742,9 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
                     const float2 b2 = __fmul2_rn(w, g[i]);
                     dB[i] = b2.x + b2.y;
                     gB = i ? __ffma2_rn(g[i], B[i], gB) : __fmul2_rn(g[i], B[i]);
-                    g[i] = decayed<PRECISE>(a[r][i], g[i]);
+                    g[i] = __fmul2_rn(a[r][i], g[i]);
+                    if (PRECISE)
+                        slice.decayed_by(i, a[r][i]);
                     const float2 q = __fmul2_rn(g[i], h[r][i]);
                     gA = i ? __ffma2_rn(q, A[i], gA) : __fmul2_rn(q, A[i]);
                     dA[i] = __ffma2_rn(q, dl, dA[i]);
@@ -719,6 +756,11 @@ __global__ void __launch_bounds__(kBwdThreads, 3) grad_kernel(const __grid_const
                     make_float4(dB[0], dB[1], dB[2], dB[3]);
                 *reinterpret_cast<float4*>(&sm.dbc[x.warp][r][1][x.cg][4 * x.ng]) =
                     make_float4(dC[0], dC[1], dC[2], dC[3]);
+            }
+            if (PRECISE) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    g[i] = slice.restored(i, A[i], g[i]);
             }
             __syncwarp();
             finish_slice(p, un, x, t + r0, r0, sm, st, dskip, dbias);

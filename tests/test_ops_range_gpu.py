@@ -189,3 +189,75 @@ def test_constant_gates_of_long_memory(cuda_device, io, form, complement):
                                        return_last_state=True)
     _, want = ref.recurrence(ref.f64(x), ref.f64(gate), form=form, complement=complement)
     each(last, want, 7.5e-5, "last")
+
+
+# ----------------------------------------------------------------------------- strong decays
+
+@pytest.mark.parametrize("segments", [1, 3])
+@pytest.mark.parametrize("N", [5, 16])
+@pytest.mark.parametrize("io", [F32, BF16])
+def test_scan_gradient_of_strong_decays(cuda_device, io, N, segments):
+    # Delta |A| from 0.01 to 33 over the states of one channel, every factor positive.  Delta A is
+    # rounded twice (33 2^-24 (1 + log2(e)) = 5e-6), the exponential adds 2^-22; the sums over 120
+    # terms of one sign and their factors at most 20 2^-24 more.
+    g = gen(8)
+    b, L, D = 2, 60, 40
+    u, delta = positive(g, b, L, D, dtype=io), (1 + 0.1 * torch.rand(b, L, D, generator=g)).to(io)
+    A = -torch.exp(torch.linspace(-4.6, 3.4, N)).expand(D, N).contiguous()
+    B, C = positive(g, b, L, N, dtype=io), positive(g, b, L, N, dtype=io)
+    dout = positive(g, b, L, D, dtype=io)
+    h0, dlast = positive(g, 1, b, D, N), positive(g, 1, b, D, N)
+    got = ops.selective_scan_bwd(*(v.cuda() for v in (dout, u, delta, A, B, C)), softplus=False,
+                                 initial_state=h0.cuda(), dlast_state=dlast.cuda(),
+                                 segments=segments)
+    leaves = [ref.f64(v).requires_grad_() for v in (A, h0)]
+    out, last = ref.scan(ref.f64(u), ref.f64(delta)[None], leaves[0], ref.f64(B)[None],
+                         ref.f64(C)[None], softplus=False, h0=leaves[1])
+    wA, w0 = torch.autograd.grad((out * ref.f64(dout)).sum() + (last * ref.f64(dlast)).sum(), leaves)
+    each(got["dA"], wA, 1e-5, "dA")
+    each(got["dinitial_state"], w0, 1e-5, "dinitial_state")
+
+
+@pytest.mark.parametrize("segments", [1, 4])
+@pytest.mark.parametrize("N", [4, 16])
+def test_scan_gradient_of_long_memories(cuda_device, N, segments):
+    # One Delta a channel at every step, memories of 300 to 2000 steps, every factor positive: an error
+    # of the decay would be multiplied by the memory (2^-24 by 2000: 1.2e-4).  The product of four decays
+    # is known to 2^-22 of its distance from one, which is what the state gets of it, and the rounding
+    # errors of a step, 2^-24 with both signs, add sqrt(1000) 2^-24 = 1.9e-6 (rms) to state and gradient.
+    g = gen(9)
+    b, L, D = 1, 3000, 32
+    memory = torch.exp(torch.empty(D, N).uniform_(5.7, 7.6, generator=g))
+    step = torch.empty(D).uniform_(0.01, 0.1, generator=g)
+    A = -1 / (memory * step[:, None])
+    u, delta = positive(g, b, L, D), step.expand(b, L, D).contiguous()
+    B, C, dout = positive(g, b, L, N), positive(g, b, L, N), positive(g, b, L, D)
+    h0 = positive(g, 1, b, D, N)
+    got = ops.selective_scan_bwd(*(v.cuda() for v in (dout, u, delta, A, B, C)), softplus=False,
+                                 initial_state=h0.cuda(), segments=segments)
+    names = ("du", "ddelta", "dA", "dB", "dC", "dinitial_state")
+    leaves = [ref.f64(v).requires_grad_() for v in (u, delta[None], A, B[None], C[None], h0)]
+    out, _ = ref.scan(*leaves[:5], softplus=False, h0=leaves[5])
+    want = torch.autograd.grad((out * ref.f64(dout)).sum(), leaves)
+    for n, w in zip(names, want):
+        if n == "ddelta":  # a difference of two large sums
+            ref.close(got[n], w[0], what=n)
+        else:
+            each(got[n], w.reshape(got[n].shape), 1.5e-5, n)
+
+
+def test_scan_gradient_of_steps_of_both_signs(cuda_device):
+    # decays of e^-6 to e^6 whose products lie near one: 60 steps, each off by at most 2^-21
+    g = gen(10)
+    b, L, D, N = 2, 60, 16, 8
+    delta = 3 * torch.where(torch.arange(L) % 2 == 0, 1.0, -1.0)[None, :, None] + \
+        0.01 * torch.rand(b, L, D, generator=g)
+    A = -torch.linspace(0.1, 2, N).expand(D, N).contiguous()
+    u, B, C, dout = (torch.randn(b, L, n, generator=g) for n in (D, N, N, D))
+    got = ops.selective_scan_bwd(*(v.cuda() for v in (dout, u, delta, A, B, C)), softplus=False,
+                                 segments=2)
+    names = ("du", "ddelta", "dA", "dB", "dC")
+    leaves = [ref.f64(v).requires_grad_() for v in (u, delta[None], A, B[None], C[None])]
+    out, _ = ref.scan(*leaves, softplus=False)
+    for n, w in zip(names, torch.autograd.grad((out * ref.f64(dout)).sum(), leaves)):
+        ref.close(got[n], w.reshape(got[n].shape), what=n)
