@@ -23,6 +23,27 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kRows = 4;  // rows of a CTA at most
 
+// Abar h + w of two states, x = Delta A log2(e).  The state is rounded token after token, in place: next
+// to one Abar counts by its distance from one, whose relative error is that of the state, where its own
+// (2^-22 with the exponential) would be multiplied by the memory.  Series to the fourth power: below
+// 1.3e-7 relative at |Delta A| = 1/16, beyond which a memory is 16 tokens at most.  (Not for infinite
+// states, which stay.)  Without it, 3000 tokens at memories of 200 to 2000: 4.7e-6 off in the mean, 2.5e-5
+// at most; with it 5e-9 and 2.5e-6, at 43.1 us for 41.4 (256 rows x 5120 channels x 16 states).
+__device__ __forceinline__ float2 next_state(float2 x, float2 h, float2 w)
+{
+    const float2 e = make_float2(ex2(x.x), ex2(x.y));
+    auto two = [](float v) { return make_float2(v, v); };
+    float2 c = __ffma2_rn(two(kLn2 * kLn2 * kLn2 * kLn2 / 24.f), x, two(kLn2 * kLn2 * kLn2 / 6.f));
+    c = __ffma2_rn(c, x, two(kLn2 * kLn2 / 2.f));
+    c = __ffma2_rn(c, x, two(kLn2));
+    c = __fmul2_rn(c, x);
+    constexpr float kMost = 0.09f;  // 1/16 in base 2
+    const bool nx = fabsf(x.x) <= kMost && fabsf(h.x) < __uint_as_float(0x7f800000u);
+    const bool ny = fabsf(x.y) <= kMost && fabsf(h.y) < __uint_as_float(0x7f800000u);
+    const float2 next = __ffma2_rn(make_float2(nx ? c.x : e.x, ny ? c.y : e.y), h, w);
+    return __fadd2_rn(next, make_float2(nx ? h.x : 0.f, ny ? h.y : 0.f));
+}
+
 // What a row brings to a lane: the states of its cells, B and C of its state group, and the inputs
 // of its channel.
 template <typename io_t, int LPC, int NS> struct Row {
@@ -207,11 +228,16 @@ __global__ void __launch_bounds__(kThreads, UNITS > 0 ? 6 : 3) step_kernel(const
             float part = 0.f;
             if (holds[s]) {
 #pragma unroll
-                for (int n = 0; n < NS; ++n)
-                    if (n < nn) {
-                        x.h[s][n] = fmaf(ex2(dl * A[s][n]), x.h[s][n], ws * B[n]);
-                        part = fmaf(x.h[s][n], C[n], part);
-                    }
+                for (int n = 0; n < NS; n += 2) {
+                    float2 v = make_float2(x.h[s][n], x.h[s][n + 1]);
+                    const float2 a = make_float2(A[s][n], A[s][n + 1]), d2 = make_float2(dl, dl);
+                    v = next_state(__fmul2_rn(a, d2), v, make_float2(ws * B[n], ws * B[n + 1]));
+                    x.h[s][n] = v.x, x.h[s][n + 1] = v.y;
+                    if (n < nn)
+                        part = fmaf(v.x, C[n], part);
+                    if (n + 1 < nn)
+                        part = fmaf(v.y, C[n + 1], part);
+                }
                 if (VEC) {
                     *reinterpret_cast<float4*>(cell + s * CP * N) =
                         make_float4(x.h[s][0], x.h[s][1], x.h[s][2], x.h[s][3]);

@@ -191,6 +191,50 @@ def test_constant_gates_of_long_memory(cuda_device, io, form, complement):
     each(last, want, 7.5e-5, "last")
 
 
+@pytest.mark.parametrize("N", [1, 4, 16, 5])
+@pytest.mark.parametrize("io", [F32, BF16])
+def test_step_of_many_tokens(cuda_device, io, N):
+    # 4000 tokens in place with one Delta a channel, memories of 300 to 2000 tokens: as above, an error
+    # of the decay itself would be multiplied by the memory.  Relative errors of Delta (2^-22), of
+    # Delta A and of 1 - a (2^-22) reach the state as they are, twice: 1e-6; the state's roundings 1.2e-5.
+    g = gen(6 + N)
+    b, D, T = 1, 64, 4000
+    memory = torch.exp(torch.empty(D, N).uniform_(5.7, 7.6, generator=g))
+    delta = torch.empty(D).uniform_(0.01, 0.1, generator=g).to(io)
+    A = -1 / (memory * delta.float()[:, None])
+    u, B = positive(g, T, b, D, dtype=io), positive(g, T, b, N, dtype=io)
+    C = torch.ones(b, N, dtype=io)
+    state = torch.zeros(b, D, N, device="cuda")
+    on = [v.cuda() for v in (u, B, C, A, delta.expand(b, D).contiguous())]
+    for t in range(T):
+        ops.selective_scan_step(on[0][t].clone(), on[4], on[3], on[1][t].clone(), on[2], state,
+                                softplus=False)
+    h = torch.zeros(b, D, N, dtype=torch.float64)
+    d64 = ref.f64(delta)[:, None]
+    a = torch.exp(d64 * ref.f64(A))
+    for t in range(T):
+        h = a * h + d64 * ref.f64(u[t])[..., None] * ref.f64(B[t])[:, None]
+    each(state, h, 1.5e-5, "state")
+
+
+@pytest.mark.parametrize("N", [1, 3, 5, 8, 16])
+def test_step_keeps_infinite_states(cuda_device, N):
+    g = gen(7)
+    b, D = 2, 40
+    state = torch.randn(b, D, N, generator=g)
+    state[0, 3, N - 1], state[1, 7, 0] = float("inf"), -float("inf")
+    u, delta = torch.randn(b, D, generator=g), torch.rand(b, D, generator=g) * 0.1
+    A = -torch.rand(D, N, generator=g) - 0.1
+    A[3, N - 1] = -30.0
+    B, C = positive(g, b, N), positive(g, b, N)
+    on = [v.cuda() for v in (u, delta, A, B, C, state)]
+    out = ops.selective_scan_step(*on, softplus=False)
+    r = [ref.f64(v) for v in (u, delta, A, B, state, C)]
+    want = torch.exp(r[1][..., None] * r[2]) * r[4] + (r[1] * r[0])[..., None] * r[3][:, None]
+    same_where_infinite(on[5], want, "state")
+    same_where_infinite(out, (want * r[5][:, None]).sum(-1), "out")
+
+
 # ----------------------------------------------------------------------------- strong decays
 
 @pytest.mark.parametrize("segments", [1, 3])
