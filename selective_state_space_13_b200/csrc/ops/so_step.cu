@@ -264,7 +264,8 @@ __global__ void __launch_bounds__(kThreads, UNITS > 0 ? 6 : 3) step_kernel(const
                     to[lane + 32 * i] = staged[lane + 32 * i];
         }
         if (active) {
-            y = fmaf(skip, u, y);
+            if (p.Dskip)  // (without, an infinite u would make NaN of y)
+                y = fmaf(skip, u, y);
             if (p.z)
                 y *= silu_f(ld1(&x.z));
             st1(static_cast<io_t*>(p.out) + at0 + r * p.D, y);

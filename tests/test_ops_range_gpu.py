@@ -224,6 +224,7 @@ def test_step_keeps_infinite_states(cuda_device, N):
     state = torch.randn(b, D, N, generator=g)
     state[0, 3, N - 1], state[1, 7, 0] = float("inf"), -float("inf")
     u, delta = torch.randn(b, D, generator=g), torch.rand(b, D, generator=g) * 0.1
+    u[1, 9] = float("inf")
     A = -torch.rand(D, N, generator=g) - 0.1
     A[3, N - 1] = -30.0
     B, C = positive(g, b, N), positive(g, b, N)
