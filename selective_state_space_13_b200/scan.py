@@ -278,20 +278,20 @@ def _check(t, name, shape, dtype, device):
         raise ValueError("%s must be contiguous" % name)
 
 
-_ws_cache = {}
-
-
-def _workspace(nbytes, device):
+def _workspace(nbytes, device, stream=None):
+    """Scratch of one call, from the caching allocator on the stream that the call runs on (a stream
+    object, a handle, or None for the current one): it goes back to that stream's pool, or that of the
+    graph being captured there, when the call has been enqueued, so that no other call in flight --
+    of another thread, on another stream, in a graph -- works on the same bytes.  (A graph captured
+    past torch.cuda.graph has to be given its workspace.)"""
     import torch
-    if torch.cuda.is_current_stream_capturing():
-        # a graph's scratch is its own: graphs may be replayed at the same time
-        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
-    buf = _ws_cache.get(key)
-    if buf is None or buf.numel() < nbytes:
-        buf = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-        _ws_cache[key] = buf
-    return buf
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else \
+            torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def selective_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=True,
@@ -374,7 +374,7 @@ def selective_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, softp
                      _ptr(conv_bias), width, _ptr(delta_scale))
     nws = selective_scan_workspace_size(shape, dmap, opts)
     if workspace is None and nws > 0:
-        workspace = _workspace(nws, device)
+        workspace = _workspace(nws, device, stream)
     wsb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = selective_scan_fwd_raw(shape, _ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
                                 _ptr(z), _ptr(delta_bias), softplus, dmap, _ptr(out),
@@ -502,7 +502,7 @@ def selective_scan_fwd_host(u, delta, A, B, C, D=None, z=None, delta_bias=None, 
     opts = make_opts(0, flags, None, _ptr(initial_state), _ptr(conv_weight), _ptr(conv_bias),
                      width, _ptr(delta_scale))
     nws = selective_scan_host_workspace_size(shape, dmap, opts, int(chunks))
-    ws = _host_workspace(nws, device) if nws > 0 else None
+    ws = _workspace(nws, device, stream) if nws > 0 else None
     st = selective_scan_fwd_host_raw(shape, _ptr(u), _ptr(delta), _ptr(A), _ptr(B), _ptr(C),
                                      _ptr(D), _ptr(z), _ptr(delta_bias), softplus, dmap, _ptr(out),
                                      _ptr(last_state), _ptr(ws), nws, int(chunks),
@@ -510,20 +510,3 @@ def selective_scan_fwd_host(u, delta, A, B, C, D=None, z=None, delta_bias=None, 
     if st != SS_OK:
         raise ScanError(st, "selective_scan_fwd_host")
     return (out, last_state) if return_last_state else out
-
-
-_host_ws = {}
-
-
-def _host_workspace(nbytes, device):
-    """The device workspace of the host-buffer call: one allocation per device, grown as needed.
-    Calls on one device are serialised on the library's streams, so they can share it as long
-    as the current stream orders a new allocation after the previous calls."""
-    import torch
-    buf = _host_ws.get(device.index)
-    if buf is None or buf.numel() < nbytes:
-        if buf is not None:
-            torch.cuda.current_stream(device).synchronize()
-        buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        _host_ws[device.index] = buf
-    return buf
