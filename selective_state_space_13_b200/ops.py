@@ -393,6 +393,15 @@ def selective_state_load(codes, scales, state, bits=8, src_slots=None, dst_slots
 
 # ----------------------------------------------------------------------------- autograd
 
+def _incoming(grad):
+    """A gradient as the library reads it: dense, from a 16-byte border on (autograd hands out views
+    that may start anywhere)."""
+    if grad is None:
+        return None
+    grad = grad.contiguous()
+    return grad if grad.data_ptr() % 16 == 0 else grad.clone()
+
+
 class _SelectiveScan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, u, delta, A, B, C, D, z, delta_bias, initial_state, softplus, dirs, H, W):
@@ -410,10 +419,10 @@ class _SelectiveScan(torch.autograd.Function):
         u, delta, A, B, C, D, z, delta_bias, initial_state = ctx.saved_tensors
         if dout is None and dlast is None:
             return (None,) * 13
-        dout = u.new_zeros(u.shape[-3:]) if dout is None else dout.contiguous()
+        dout = u.new_zeros(u.shape[-3:]) if dout is None else _incoming(dout)
         g = selective_scan_bwd(dout, u, delta, A, B, C, D=D, z=z, delta_bias=delta_bias,
-                               initial_state=initial_state,
-                               dlast_state=None if dlast is None else dlast.contiguous(), **ctx.call)
+                               initial_state=initial_state, dlast_state=_incoming(dlast),
+                               **ctx.call)
         return tuple(g[n] for n in ("du", "ddelta", "dA", "dB", "dC", "dD", "dz", "ddelta_bias",
                                     "dinitial_state")) + (None,) * 4
 
@@ -442,10 +451,9 @@ class _GatedRecurrence(torch.autograd.Function):
         x, gate, gate_bias, initial_state, out = ctx.saved_tensors
         if dout is None and dlast is None:
             return (None,) * 7
-        dout = torch.zeros_like(x) if dout is None else dout.contiguous()
+        dout = torch.zeros_like(x) if dout is None else _incoming(dout)
         return gated_recurrence_bwd(dout, x, gate, out, gate_bias=gate_bias,
-                                    initial_state=initial_state,
-                                    dlast_state=None if dlast is None else dlast.contiguous(),
+                                    initial_state=initial_state, dlast_state=_incoming(dlast),
                                     **ctx.call) + (None,) * 3
 
 
