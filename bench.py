@@ -126,11 +126,12 @@ def code_without_comments(text: str) -> str:
 
 
 def kernel_source_digest() -> str:
-    """Digest of the CUDA library's code (sources and headers, comments ignored): the ncu
-    record in profiles/traffic.json applies only while it matches."""
+    """Digest of the scan kernels' code (comments ignored; not of the host's entry points, which can
+    change without changing what a launch counts): the ncu record in profiles/traffic.json applies
+    only while it matches."""
     from selective_state_space_13_b200 import build as b
     h = hashlib.sha256()
-    for f in b.SOURCES + b.HEADERS:
+    for f in b.KERNEL_FILES:
         with open(f, encoding="utf-8") as fh:
             h.update(os.path.basename(f).encode())
             h.update(code_without_comments(fh.read()).encode())

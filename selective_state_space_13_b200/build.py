@@ -18,11 +18,14 @@ ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libss_b200.so")
 PROBE_LIB = os.path.join(PKG, "libss_probe.so")  # pipe-throughput probes of the benchmark
 PROBE_SOURCES = sorted(glob.glob(os.path.join(PKG, "csrc", "probe", "*.cu")))
-# the scan itself (the code that the recorded profiles of the scan belong to) ...
+# the scan itself ...
 SOURCES = sorted(glob.glob(os.path.join(PKG, "csrc", "*.cu")))
 HEADERS = sorted(glob.glob(os.path.join(PKG, "csrc", "*.h")) +
                  glob.glob(os.path.join(PKG, "csrc", "*.cuh")) +
                  [os.path.join(ROOT, "include", "selective_scan.h")])
+# (of these, what its kernels are made of: the code whose counters profiles/traffic.json records)
+KERNEL_FILES = sorted(glob.glob(os.path.join(PKG, "csrc", "ss_scan*.cu"))) + [
+    os.path.join(PKG, "csrc", n) for n in ("ss_device.cuh", "ss_internal.h", "ss_scan_kernels.cuh")]
 # ... and the operators around it, in the same library
 OPS_SOURCES = sorted(glob.glob(os.path.join(PKG, "csrc", "ops", "*.cu")))
 OPS_HEADERS = sorted(glob.glob(os.path.join(PKG, "csrc", "ops", "*.h")) +
