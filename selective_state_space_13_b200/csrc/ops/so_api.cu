@@ -48,8 +48,8 @@ ss_status check_shape(const ss_shape* s)
 }
 
 // The stream has to belong to the current device.  While a stream is being captured the runtime
-// refuses to say which device it belongs to (and the question would end the capture), so the
-// launches themselves refuse a foreign stream then.
+// refuses to say which device it belongs to (and the question would end the capture): it is not
+// checked then, and a foreign stream is left to the launches to refuse.
 ss_status check_stream(cudaStream_t st)
 {
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
@@ -155,11 +155,13 @@ struct BwdPlan {
 
 // Automatic segments of the gradient.  `units` (direction, batch row, channel tile) CTAs for each
 // segment fill the kBwdSlots CTAs that fit on a B200 (3 on each of 148 SMs) in whole waves, so S
-// segments take ceil(units S / slots) / S of a whole sequence's time; a step takes about 0.3 us, any
-// split costs about 15% more work (the segment products, the checkpoints' shift), and every wave
-// folds the other segments' states (0.2 us for each) and has its ends (2.4 us).  Measured: 8 x 2048 x 1536 (192 units) 1434 us unsplit, 923
-// at S = 2, 752 at 9, 758 at 16, 795 at 23, 828 at 30; 2 x 333 x 72 in fp32 (4 units) 232 us unsplit, 108 at 4, 70 at 20, 68 at 40;
-// 64 x 197 x 768 in two directions (1536 units) 601 us unsplit, more with any split.
+// segments take ceil(units S / slots) / S of a whole sequence's time; a step takes 0.7 us, any split
+// costs about 15% more work (the segment products, the checkpoints' shift), and every wave folds the
+// other segments' states (some 0.47 us for each) and has its ends (5.6 us).  Measured, and from that
+// rule: 8 x 2048 x 1536 (192 units) 1434 us unsplit (1434), 923 at S = 2 (831), 752 at 9 (772), 758 at 16
+// (813), 795 at 23 (880), 828 at 30 (969); 2 x 333 x 72 in fp32 (4 units) 232 us unsplit (233), 108 at 4
+// (74), 70 at 20 (28), 68 at 40 (31): what a call takes besides is not in it; 64 x 197 x 768 in two
+// directions (1536 units) 601 us unsplit (552), more with any split.  Its choices are near the best.
 constexpr int64_t kBwdSlots = 3 * 148;
 constexpr int64_t kBwdMinSteps = 16;
 constexpr int64_t kBwdMostAuto = 256;
@@ -167,10 +169,10 @@ constexpr int64_t kBwdMostAuto = 256;
 int64_t bwd_segments(int64_t units, int64_t L)
 {
     int64_t best = 1;
-    double least = 0.3 * static_cast<double>(L * ceil_div(units, kBwdSlots));
+    double least = 0.7 * static_cast<double>(L * ceil_div(units, kBwdSlots));
     for (int64_t S = 2; S <= kBwdMostAuto && S <= L / kBwdMinSteps; ++S) {
         const double waves = static_cast<double>(ceil_div(units * S, kBwdSlots));
-        const double cost = waves * (0.345 * static_cast<double>(L) / S + 0.2 * S + 2.4);
+        const double cost = waves * (0.805 * static_cast<double>(L) / S + 7. / 15. * S + 5.6);
         if (cost < 0.999 * least) {
             least = cost;
             best = S;

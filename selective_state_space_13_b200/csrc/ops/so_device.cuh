@@ -26,7 +26,8 @@ __device__ __forceinline__ float ex2(float x)
 // ex2.approx errs low: over 2^24 arguments in each decade, the mean of its relative error is
 // -0.6e-8 to -2.2e-8 for -0.5 < x < 0 (root mean square 3e-8).  A random error of a decay averages
 // out over a state's memory, a mean does not; 2e-8 more in the argument leaves at most 0.8e-8 of it,
-// and ex2 of 2e-8 itself is exactly 1, so that a step of zero still keeps the state.
+// and ex2 of 2e-8 itself is exactly 1, so that a step of zero still keeps the state.  (The scan's
+// gradient with bf16 io; the others hold their decays more closely.)
 constexpr float kDecayShift = 2e-8f;
 
 __device__ __forceinline__ float rcp(float x)
@@ -64,7 +65,7 @@ __device__ __forceinline__ float sigmoid_f(float x) { return rcp(1.f + ex2(-x * 
 
 __device__ __forceinline__ float silu_f(float x) { return x * sigmoid_f(x); }
 
-// 1 - exp(x) for x <= 0 (any x): Taylor to x^8 for |x| <= 0.35 (truncation below 3e-10
+// 1 - exp(x) for x <= 0 (any x): Taylor to x^8 for |x| <= 0.35 (truncation below 8e-10
 // relative), so that decays near one keep the relative accuracy of 1 - a.
 __device__ __forceinline__ float one_minus_exp(float x, float e)
 {

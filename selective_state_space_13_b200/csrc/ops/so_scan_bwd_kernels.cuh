@@ -8,11 +8,12 @@
 // A CTA of 4 warps owns 64 channels of one (direction, batch row, segment), a warp 16 of them, a
 // thread 2 adjacent channels x 4 states: 4 lanes make a channel (for N up to 8: 128, 32, and 2 lanes;
 // SO_STATE_GROUPS says which, one translation unit each).  The two channels are the halves
-// of every packed f32x2 operation, so Delta, Delta u and dy come out of shared memory as pairs and
-// B and C as duplicated pairs, with no moves to build operands.  The sums over states (y, sum g B,
-// sum g A h) and over channels (dB, dC) go through shared memory that is private to the warp: a
-// lane stores its partial sums once, and the lane that finishes a (step, channel pair) or a
-// (step, 4 states) adds them up, which costs fewer instructions than a butterfly of shuffles.
+// of every packed f32x2 operation, so Delta, Delta u and dy come out of shared memory as pairs; B and C
+// are scalars there, which a packed operation takes for both halves without moves.  The sums over
+// states (y, sum g B, sum g A h) and over channels (dB, dC) go through shared memory that is private to
+// the warp: a lane stores its partial sums once, and the lane that finishes a (step, channel pair) or a
+// (step, 4 states) adds them up, which costs fewer instructions than a full butterfly of shuffles (one
+// that halves what it keeps at every stage is not tried).
 // Warps meet twice per tile of kTL steps: when its rows have landed and B and C are converted.
 //
 // Sequences are cut into S segments when there are too few CTAs.  The summary sweep then starts

@@ -11,8 +11,9 @@
 // has all states of its channel; they, and B and C, pass through shared memory, so that the accesses
 // to memory are contiguous there too (directly: N = 15, 111 us for those rows).  A CTA
 // keeps its channels' parameters (A alone is as long as a row's state) for up to kRows rows.  Measured
-// for those 256 rows: 42.1 us with 4 rows and 24 warps on an SM, 43.3 with 2 rows, 49 with 8; 51 us with
-// 16 warps and the next row's loads ahead of the arithmetic (70% of the measured HBM rate).
+// for those 256 rows, before decays next to one were taken by their distance from it: 42.1 us with 4 rows
+// and 24 warps on an SM, 43.3 with 2 rows, 49 with 8; 51 us with 16 warps and the next row's loads ahead
+// of the arithmetic.  Now 43.1 us, 68% of the measured HBM rate (N = 15: 59.5).
 #include "so_device.cuh"
 
 namespace so {

@@ -248,8 +248,8 @@ ss_status selective_scan_fwd(const ss_shape* shape, const void* u, const void* d
 
     cudaStream_t strm = static_cast<cudaStream_t>(stream);
     // the stream must belong to the current device, whose error word the kernels report to; while
-    // it is being captured the runtime refuses to say (and asking would end the capture), so the
-    // launches themselves refuse a foreign stream then
+    // it is being captured the runtime refuses to say (and asking would end the capture): it is not
+    // checked then, and a foreign stream is left to the launches to refuse
     auto stream_on_current_device = [&]() -> ss_status {
         cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
         if (cudaStreamIsCapturing(strm, &cap) != cudaSuccess)

@@ -85,7 +85,7 @@ __device__ __forceinline__ float log1p_unit(float e)
 }
 
 // exp(x) - 1 with relative accuracy ~1e-7 near 0 (Taylor to x^8 for |x| <= 0.35, truncation
-// < 3e-10 relative), exp through ex2 elsewhere.
+// < 8e-10 relative), exp through ex2 elsewhere.
 __device__ __forceinline__ float expm1_acc(float x)
 {
     float p = 1.f / 40320.f;
