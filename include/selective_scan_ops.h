@@ -139,7 +139,9 @@ ss_status selective_scan_bwd(const ss_shape* shape, const void* u, const void* d
  *   slots        [batch] int32 device array, or NULL for slot r = row r.  A row whose slot is
  *                outside [0, num_slots) is padding: its out row and every state stay as they
  *                were.  Of several rows that name one slot, the lowest takes it and the others
- *                are padding.
+ *                are padding.  Every row looks through the entries before its own, so the look-ups
+ *                grow with the square of the rows (nothing beside the states for some thousand of
+ *                them); with a list, batch is at most 2^20 (SS_ERR_SHAPE)
  *   conv_weight  [D, conv_width] fp32 (conv_width 1..SS_MAX_CONV_WIDTH) or NULL; conv_bias [D]
  *                fp32 or NULL; tap conv_width-1 multiplies this token's u
  *   conv_state   [num_slots, conv_width-1, D] io: the inputs before this token, oldest first, in
@@ -170,7 +172,8 @@ ss_status selective_scan_step(const ss_shape* shape, int64_t num_slots, const vo
  *   state   [state_slots, D, N] fp32, 16-byte aligned
  *   src_slots, dst_slots  [rows] int32 device arrays, or NULL for slot r = row r; rows with a
  *           slot outside its pool are skipped, and of several rows with one destination the
- *           lowest is taken
+ *           lowest is taken; with a list of destinations rows is at most 2^20 (SS_ERR_SHAPE), as in
+ *           the step
  */
 ss_status selective_state_store(int64_t rows, int64_t dim, int64_t dstate, int32_t bits,
                                 const float* state, int64_t state_slots,

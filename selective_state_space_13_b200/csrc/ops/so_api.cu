@@ -13,6 +13,9 @@ namespace {
 
 constexpr int64_t kMaxI32 = (int64_t{1} << 31) - 1;
 constexpr int kMaxSegments = 1024;
+// Rows of a call with a list of slots that must not repeat: every row looks through the list before it,
+// so that the look-ups grow with the square of the rows (2^20 of them: by estimate 0.2 s a channel tile).
+constexpr int64_t kMostListedRows = int64_t{1} << 20;
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -534,7 +537,8 @@ ss_status selective_scan_step(const ss_shape* shape, int64_t num_slots, const vo
     if (st != SS_OK)
         return st;
     const int64_t b = shape->batch, D = shape->dim;
-    if (shape->seqlen != 1 || num_slots < 1 || num_slots > kMaxI32 || (!slots && num_slots < b))
+    if (shape->seqlen != 1 || num_slots < 1 || num_slots > kMaxI32 || (!slots && num_slots < b) ||
+        (slots && b > kMostListedRows))
         return SS_ERR_SHAPE;
     if (conv_weight ? conv_width < 1 || conv_width > SS_MAX_CONV_WIDTH
                     : conv_width != 0 || conv_bias || conv_state)
@@ -587,7 +591,7 @@ static ss_status state_call(bool load, int64_t rows, int64_t dim, int64_t dstate
         return SS_ERR_UNSUPPORTED;
     const int64_t from = load ? cache_slots : state_slots, to = load ? state_slots : cache_slots;
     if (from < 1 || to < 1 || from > kMaxI32 || to > kMaxI32 || (!src && from < rows) ||
-        (!dst && to < rows) || ceil_div(dim, 32) * rows > kMaxI32)
+        (!dst && to < rows) || ceil_div(dim, 32) * rows > kMaxI32 || (dst && rows > kMostListedRows))
         return SS_ERR_SHAPE;
     if (rows * dim > 0 && ((!state_in && !state_out) || !codes || !scales))
         return SS_ERR_NULL;

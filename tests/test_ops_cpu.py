@@ -187,3 +187,18 @@ def test_binding_refuses_host_tensors():
                                   torch.zeros(2, 8))
     with pytest.raises(ValueError):
         ops.selective_scan_bwd(x, x, x, torch.zeros(8, 4), x, x)
+
+
+def test_long_slot_lists_are_refused():
+    # every row looks through the list before it: 2^20 rows are the most
+    most = 1 << 20
+    assert step(sh=shape(batch=most + 1, seqlen=1, dim=8, dstate=1), num_slots=4) == 2
+    lib = ops.load()
+    for src, dst in ((None, FAKE), (FAKE, FAKE)):
+        assert lib.selective_state_store(most + 1, 8, 1, 8, FAKE, most + 1, src, FAKE, FAKE,
+                                         most + 1, dst, None) == 2
+        assert lib.selective_state_load(most + 1, 8, 1, 8, FAKE, FAKE, most + 1, src, FAKE,
+                                        most + 1, dst, None) == 2
+    # ... and what is refused for another reason keeps it
+    assert step(sh=shape(batch=most + 1, seqlen=1, dim=8, dstate=1), slots=None,
+                num_slots=most + 1, u=None) == 1
