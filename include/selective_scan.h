@@ -238,8 +238,8 @@ ss_status selective_scan_device_status(void* stream, int32_t clear);
  *     with that device current); make that first call before any stream capture.
  *   - All calls share the one array, which keeps the last call's contents.  Nothing in it has to
  *     start at zero: every value a call reads from it was written earlier by the same call.
- *     Calls whose work overlaps on the GPU (other streams, other host threads) race on the
- *     array; order them, for example on one stream.
+ *     Calls whose work overlaps on the GPU (other streams, other host threads, graphs that hold
+ *     such calls and are replayed) race on the array; order them, for example on one stream.
  */
 ss_status selective_scan_fwd_noalloc(const ss_shape* shape, const void* u, const void* delta,
                                      const float* A, const void* B, const void* C,

@@ -35,7 +35,10 @@ extern "C" {
  *   out_t = h_t
  *
  * elementwise per channel, along t = 0..L-1 (SS_DIR_FWD) or t = L-1..0 (SS_DIR_REV).  The state
- * is held in fp32; out is rounded to the io type once.
+ * is held in fp32; out is rounded to the io type once.  Both a and 1 - a are relatively accurate (2^-21
+ * and |s_t| 2^-22; the sigmoid down to 2^-100), so that a memory of thousands of steps keeps its length
+ * and a gate that closes leaves a h_{t-1} and nothing else.  An infinite state stays: no decay is below 2^-149, that of
+ * a gate of -inf included.
  */
 typedef enum { SS_GATE_SIGMOID = 0, SS_GATE_EXP = 1 } ss_gate_form;
 
@@ -94,6 +97,9 @@ ss_status gated_recurrence_bwd(const ss_shape* shape, const ss_recurrence_opts* 
  *   dz_p  = dout_p silu'(z_p) sum_k y_k           ddelta_bias = sum_{b,t} ddelta_t
  *
  * The state and every sum are fp32.  Gradients have the shapes and types of what they belong to.
+ * The workspace is large: one state in four, 4 bytes x K x batch x L / 4 x D x N (N padded to 8 or 16),
+ * and the partial sums of dB and dC over 1024 / N channels; 507 MB for 8 x 2048 x 1536 x 16, 12.8 GB
+ * for 1 x 131072 x 5120 x 16.
  */
 typedef struct {
     void* du;              /* [batch, L, D] io ([K, batch, L, D] with SS_FLAG_U_PER_DIRECTION)  */

@@ -4,8 +4,9 @@ The functions carry the C names -- selective_scan_bwd, gated_recurrence_fwd, gat
 selective_scan_step, selective_state_store, selective_state_load -- and only marshal arguments:
 they check shapes, dtypes and devices, allocate outputs and workspaces that the caller did not pass
 (from PyTorch's allocator, on the current stream) and call the library on the current CUDA stream
-of the tensors' device, which has to be the current device.  selective_scan and gated_recurrence
-wrap forward and gradient for torch.autograd.  There is no CPU path.
+of the tensors' device, which has to be the current device.  Outputs, and what is updated in place,
+must not overlap inputs.  selective_scan and gated_recurrence wrap forward and gradient for
+torch.autograd.  There is no CPU path.
 
 A training step through those two can be captured into a CUDA graph after one eager step.  Nothing
 of an eager graph of the same leaves (an output or loss of theirs) may then be alive: PyTorch keeps
