@@ -238,8 +238,10 @@ def selective_scan_bwd(dout, u, delta, A, B, C, D=None, z=None, delta_bias=None,
     with the shape and dtype of its input and None where the input is None.  The exact ZOH, int8
     delta and the fused convolution have no gradient here.
     """
-    device = _device_of(u, "u")
     K = len(dirs)
+    # (the C call refuses int8 delta with its flag)
+    _scan._check_flags(int(flags) & ~_scan.SS_FLAG_DELTA_INT8, K, u, delta, A)
+    device = _device_of(u, "u")
     if not 1 <= K <= SS_MAX_DIRS:
         raise ValueError("1 to %d directions, got %d" % (SS_MAX_DIRS, K))
     if u.dim() == 4 and u.shape[0] == K:

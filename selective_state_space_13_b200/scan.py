@@ -294,6 +294,21 @@ def _workspace(nbytes, device, stream=None):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
+def _check_flags(flags, K, u, delta, A):
+    """The flags that speak of shapes or types are set from the tensors; given by hand against them,
+    they would make the kernels read behind a tensor's end."""
+    import torch
+    flags, wrong = int(flags), 0
+    if K > 1:
+        wrong |= SS_FLAG_U_PER_DIRECTION if u.dim() == 3 else 0
+        wrong |= SS_FLAG_PARAMS_PER_DIRECTION if A.dim() == 2 else 0
+    wrong |= 0 if delta.dtype == torch.int8 else SS_FLAG_DELTA_INT8
+    if flags & wrong & ~SS_FLAG_DELTA_INT8:
+        raise ValueError("flags name an input or parameters per direction that are given once")
+    if flags & wrong:
+        raise ValueError("flags name int8 delta codes, delta is %s" % delta.dtype)
+
+
 def selective_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=True,
                        dirs=(SS_DIR_FWD,), H=0, W=0, out=None, last_state=None,
                        return_last_state=False, workspace=None, stream=None, segments=0,
@@ -317,6 +332,7 @@ def selective_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, softp
     import torch
     device = u.device
     K = len(dirs)
+    _check_flags(flags, K, u, delta, A)
     if u.dim() == 4 and u.shape[0] == K:
         flags = int(flags) | SS_FLAG_U_PER_DIRECTION
     elif u.dim() != 3:
@@ -444,6 +460,7 @@ def selective_scan_fwd_host(u, delta, A, B, C, D=None, z=None, delta_bias=None, 
     if device is None:
         device = torch.device("cuda", torch.cuda.current_device())
     K = len(dirs)
+    _check_flags(flags, K, u, delta, A)
     if delta.dim() == 3:
         delta = delta.unsqueeze(0)
     if B.dim() == 3:
