@@ -306,3 +306,51 @@ def test_scan_gradient_of_steps_of_both_signs(cuda_device):
     out, _ = ref.scan(*leaves, softplus=False)
     for n, w in zip(names, torch.autograd.grad((out * ref.f64(dout)).sum(), leaves)):
         ref.close(got[n], w.reshape(got[n].shape), what=n)
+
+
+# ----------------------------------------------------------------------------- growth
+
+@pytest.mark.parametrize("complement", [False, True])
+@pytest.mark.parametrize("io", [F32, BF16])
+def test_gates_that_grow(cuda_device, io, complement):
+    # "normally <= 0": a > 1 is the same recurrence; 200 steps of up to e^0.3, about e^20 in all.  Each
+    # factor is off by at most 2^-22 and four roundings, over 200 steps 1e-4 of a state at the most, a
+    # tenth of that with errors of both signs: within the usual bound.
+    g = gen(11)
+    b, L, D = 2, 200, 24
+    gate = (0.1 + 0.1 * torch.randn(b, L, D, generator=g)).to(io)
+    x, dout = torch.randn(b, L, D, generator=g).to(io), torch.randn(b, L, D, generator=g).to(io)
+    h0, dlast = torch.randn(b, D, generator=g), torch.randn(b, D, generator=g)
+    on = [v.cuda() for v in (x, gate, h0, dout, dlast)]
+    out, last = ops.gated_recurrence_fwd(on[0], on[1], initial_state=on[2], form="exp",
+                                         complement=complement, return_last_state=True)
+    r = [ref.f64(v) for v in (x, gate, h0, dout, dlast)]
+    want, wlast = ref.recurrence(r[0], r[1], h0=r[2], form="exp", complement=complement)
+    ref.close(out, want, what="out")
+    ref.close(last, wlast, what="last")
+    got = ops.gated_recurrence_bwd(on[3], on[0], on[1], out, initial_state=on[2], dlast_state=on[4],
+                                   form="exp", complement=complement)
+    wants = ref.recurrence_grads(r[3], r[0], r[1], ref.f64(out), h0=r[2], dlast=r[4], form="exp",
+                                 complement=complement)
+    for name, a, w in zip(("dx", "dgate", "dbias", "dh0"), got, wants):
+        if a is not None:
+            ref.close(a, w, what=name)
+
+
+@pytest.mark.parametrize("io", [F32, BF16])
+def test_scan_gradient_of_growth(cuda_device, io):
+    # A of both signs: decays of e^-0.5 to e^0.15 a step, 60 steps, as above
+    g = gen(12)
+    b, L, D, N = 2, 60, 16, 8
+    delta = (0.5 + 0.5 * torch.rand(b, L, D, generator=g)).to(io)
+    A = torch.linspace(-0.5, 0.15, N).expand(D, N).contiguous()
+    u, B, C, dout = (torch.randn(b, L, n, generator=g).to(io) for n in (D, N, N, D))
+    h0 = torch.randn(1, b, D, N, generator=g)
+    for segments in (1, 3):
+        got = ops.selective_scan_bwd(*(v.cuda() for v in (dout, u, delta, A, B, C)),
+                                     softplus=False, initial_state=h0.cuda(), segments=segments)
+        names = ("du", "ddelta", "dA", "dB", "dC", "dinitial_state")
+        leaves = [ref.f64(v).requires_grad_() for v in (u, delta[None], A, B[None], C[None], h0)]
+        out, _ = ref.scan(*leaves[:5], softplus=False, h0=leaves[5])
+        for n, w in zip(names, torch.autograd.grad((out * ref.f64(dout)).sum(), leaves)):
+            ref.close(got[n], w.reshape(got[n].shape), what=n)
