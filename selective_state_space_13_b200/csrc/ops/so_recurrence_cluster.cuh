@@ -18,16 +18,18 @@
 // A step is a h + w, with a itself: a gate that closes leaves nothing of the old state but a h, and an
 // infinite state stays infinite.  Next to a decay of one that would lose 2^-25 of the state (and the
 // exponential's error) at every step, which a memory of 1000 steps multiplies.  It does not come to
-// that, because states go from one warp's steps to the next through the products P alone: a product
-// gets back what its factors lost, by 1 - a, which is known to its own accuracy (sigmoid: P (1 + sum of
-// (1 - a) - what 1 - a is); exp: the exponential of the sum).
+// that, because states go from one warp's steps to the next through the products P alone, and next to one
+// these are taken from U = 1 - P, which is relatively accurate: sigmoid, U' = U + P (1 - a); exp, from the
+// sum of the gates.  Where a CTA walks a column alone, as it does in calls of a few steps, the state
+// behind its tile is (h - U h) + H, so that token after token loses nothing of a long memory either.
 //
-// Measured on B200 (8 x 2048 x 1536 bf16): 36.2 us among other passes, 64% of the measured HBM rate.
+// Measured on B200 (8 x 2048 x 1536 bf16): 34.8 us among other passes, 66% of the measured HBM rate.
 // With an event around each pass, and a - 1 alone: CTAs of 4 warps, 16 steps a warp, 36.9 us; of 8 warps
 // 41 us; of 16 warps with 8 steps 47 us (the barriers cost more than the shorter chains give).  More
 // than about three CTAs on an SM run slower, not faster.  TMA boxes for the rows: the same times.
-// a - 1 alone, which is wrong where gates close, took 33.0 us among other passes where this takes 36.0
-// (1 x 131072 x 5120: 730 and 786); a = k + m with k = 0 or 1 for every step, as right as this, 39.0 (862).
+// a - 1 alone, which is wrong where gates close, took 33.0 us among other passes (1 x 131072 x 5120: 731,
+// here 756); a = k + m with k = 0 or 1 for every step, as right as this, 39.0 (862); P corrected by what
+// every factor had lost, 36.0 (786).
 #pragma once
 
 #include <type_traits>
@@ -55,6 +57,7 @@ template <typename io_t, bool BWD> struct RecSmem {
     io_t raw[2][T::kTensors][T::kRows][kRecCh];  // [stage][tensor], rows in the order of the steps
     float4 warp_map[kRecWarps][32];  // a warp's steps; then what lies before them in the tile
     float2 start[32];                // the state before the tile
+    float2 warp_u[kRecWarps][32];    // U of a warp's steps (a CTA alone)
     float4 cta_map[2][kRecMostCluster][32];  // written by every CTA of the cluster
     uint64_t maps[2];  // the maps of the cluster's CTAs have landed
 };
@@ -102,11 +105,23 @@ __device__ __forceinline__ void decays_of(float2 gate, float2 bias, float2& a, f
     }
 }
 
-// exp(x), next to one to half a step.
-__device__ __forceinline__ float exp_of(float x)
+// U and P of decays whose logarithms add up to `sum`.
+__device__ __forceinline__ void product_of_logs(float sum, float& u, float& p)
 {
-    const float e = ex2(x * kLog2e);
-    return fabsf(x) <= 0.35f ? 1.f - one_minus_exp(x, e) : e;
+    p = ex2(sum * kLog2e);
+    u = one_minus_exp(sum, p);
+}
+
+// P from U = 1 - P where that is more accurate.
+__device__ __forceinline__ bool near_one(float u) { return fabsf(u) <= 0.5f; }
+__device__ __forceinline__ float from_u(float u, float p) { return near_one(u) ? 1.f - u : p; }
+
+// P h + H of one channel, from U where P is near one; an infinite h stays.
+__device__ __forceinline__ float through_u(float p, float u, float H, float h)
+{
+    const bool finite = fabsf(h) < __uint_as_float(0x7f800000u);
+    const float next = fmaf(-u, h, H) + h;
+    return near_one(u) && finite ? next : fmaf(p, h, H);
 }
 
 // 16 bytes global -> shared, zeros where !valid.
@@ -284,7 +299,7 @@ __global__ void __launch_bounds__(kRecThreads, 3)
                 return P2::f(v[i]);
         };
         float2 P = one, H = make_float2(0.f, 0.f);
-        float2 lost = make_float2(0.f, 0.f);  // exp: the sum of the gates
+        float2 U = make_float2(0.f, 0.f);  // (exp: until the end the sum of the gates)
         // steps behind the end keep the state
         auto compose_steps = [&](bool whole) {
 #pragma unroll
@@ -299,12 +314,13 @@ __global__ void __launch_bounds__(kRecThreads, 3)
                 const bool inside = whole || s0 + i < t1;
                 if (!inside) {
                     a[i] = one;
+                    r = make_float2(0.f, 0.f);
                     v[i] = {};
                 }
-                if (inside && FORM == SS_GATE_EXP)
-                    lost = __fadd2_rn(lost, gate);
+                if (FORM == SS_GATE_SIGMOID)
+                    U = __ffma2_rn(r, P, U);
                 else if (inside)
-                    lost = __fadd2_rn(lost, __ffma2_rn(r, minus, __ffma2_rn(a[i], minus, one)));
+                    U = __fadd2_rn(U, gate);
                 if (BWD)
                     H = __fmul2_rn(a[i], __fadd2_rn(H, in(i)));
                 else
@@ -312,11 +328,12 @@ __global__ void __launch_bounds__(kRecThreads, 3)
                 if (FORM == SS_GATE_SIGMOID)
                     P = __fmul2_rn(a[i], P);
             }
-            if (FORM == SS_GATE_SIGMOID)
-                P = __ffma2_rn(P, lost, P);
-            else
-                P = make_float2(exp_of(lost.x), exp_of(lost.y));
-            P = at_least(P, kLeast);
+            if (FORM == SS_GATE_EXP) {
+                const float2 sum = U;
+                product_of_logs(sum.x, U.x, P.x);
+                product_of_logs(sum.y, U.y, P.y);
+            }
+            P = at_least(make_float2(from_u(U.x, P.x), from_u(U.y, P.y)), kLeast);
         };
         const bool whole = s0 + N <= t1;
         if (whole)
@@ -324,6 +341,8 @@ __global__ void __launch_bounds__(kRecThreads, 3)
         else
             compose_steps(false);
         sm.warp_map[warp][lane] = make_float4(P.x, P.y, H.x, H.y);
+        if (cs == 1)
+            sm.warp_u[warp][lane] = U;
         if (!BWD) {
             __syncwarp();  // the rows are in registers: their stage takes those of two rounds on
             load(m + 2);
@@ -336,6 +355,8 @@ __global__ void __launch_bounds__(kRecThreads, 3)
             for (int w = 0; w < kRecWarps; ++w) {
                 const float4 f = sm.warp_map[w][lane];
                 sm.warp_map[w][lane] = all;
+                if (cs == 1)
+                    U = w ? __ffma2_rn(sm.warp_u[w][lane], make_float2(all.x, all.y), U) : U;
                 all = compose(f, all);
             }
             float2 h = carry;
@@ -364,7 +385,8 @@ __global__ void __launch_bounds__(kRecThreads, 3)
                         product = at_least(__fmul2_rn(product, make_float2(f.x, f.y)), kLeast);
                     }
             } else {
-                carry = through(all, carry);
+                carry = make_float2(through_u(all.x, U.x, all.z, carry.x),
+                                    through_u(all.y, U.y, all.w, carry.y));
                 product = at_least(__fmul2_rn(product, make_float2(all.x, all.y)), kLeast);
             }
             sm.start[lane] = h;

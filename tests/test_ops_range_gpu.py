@@ -177,8 +177,8 @@ def test_constant_gates_of_long_memory(cuda_device, io, form, complement):
     # One gate a channel at every step, memories of 500 to 2000 steps: an error of the decay itself
     # comes back multiplied by the memory.  1 - a has a relative error of 2^-22, which is that of the
     # state; rounding the state twice a step with random inputs adds sqrt(1000) 2 2^-25 = 1.9e-6 (rms),
-    # six times that at most.  A product of the decays of some steps is rounded by at most half a step
-    # of [1/2, 1), 2^-25, at every factor, each time in the same way: 2000 2^-25 = 6e-5.
+    # six times that at most.  The product of the decays of 8 or 16 steps is rounded once, by at most half
+    # a step of [1/2, 1), 2^-25, each time in the same way: 2000 / 8 2^-25 = 7.5e-6.
     g = gen(5)
     b, L, D = 1, 8000, 256
     memory = torch.exp(torch.empty(D).uniform_(6.2, 7.6, generator=g))
@@ -188,7 +188,28 @@ def test_constant_gates_of_long_memory(cuda_device, io, form, complement):
     _, last = ops.gated_recurrence_fwd(x.cuda(), gate.cuda(), form=form, complement=complement,
                                        return_last_state=True)
     _, want = ref.recurrence(ref.f64(x), ref.f64(gate), form=form, complement=complement)
-    each(last, want, 7.5e-5, "last")
+    each(last, want, 2.5e-5, "last")
+
+
+@pytest.mark.parametrize("chunk", [1, 3])
+@pytest.mark.parametrize("io", [F32, BF16])
+@pytest.mark.parametrize("form", ["sigmoid", "exp"])
+def test_recurrence_token_after_token(cuda_device, form, io, chunk):
+    # the same in calls of one or three steps, the state handed on: 3000 roundings of a decay, 2^-25,
+    # all in the same way, would be 6e-5 of a memory of 2000
+    g = gen(13)
+    b, L, D = 2, 3000, 64
+    memory = torch.exp(torch.empty(D).uniform_(5.7, 7.6, generator=g))
+    s = torch.log(memory - 1) if form == "sigmoid" else -1 / memory
+    gate = s.expand(b, chunk, D).to(io).contiguous()
+    x = positive(g, L // chunk, b, chunk, D, dtype=io)
+    on, h = (x.cuda(), gate.cuda()), torch.zeros(b, D, device="cuda")
+    for i in range(L // chunk):
+        _, h = ops.gated_recurrence_fwd(on[0][i], on[1], initial_state=h, form=form,
+                                        return_last_state=True)
+    whole = ref.f64(x).permute(1, 0, 2, 3).reshape(b, L, D)
+    _, want = ref.recurrence(whole, ref.f64(gate[:, :1]).expand(b, L, D), form=form)
+    each(h, want, 1.5e-5, "state")
 
 
 @pytest.mark.parametrize("N", [1, 4, 16, 5])
