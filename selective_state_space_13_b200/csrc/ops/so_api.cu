@@ -79,9 +79,9 @@ struct RecPlan {
 // CTAs in the cluster of a column of 64 channels.  A B200 runs about three of the recurrence's CTAs
 // on each of its 148 SMs best, so a launch takes as long as its whole waves of 444: the cluster is
 // the size that fills them best, an eighth dearer for every CTA more that has to be heard.  Measured at
-// 1, 2, 4, 6 and 8 CTAs (us, bf16): 8 x 2048 x 1536 (192 columns) 43.1, 36.3, 39.3, 45.3, 48.6; 16 x 2048
-// x 1536: 57.8, 65.1, 71.2, 80.8, 90.3; 16 x 1024 x 1024: 24.7, 29.7, 31.9, 36.5, 41.4; 1 x 32768 x 5120:
-// 440, 347, 242, 259, 247; 4 x 8192 x 1536: 114, 92, 66, 80, 74; 3 was slower than its neighbours.
+// 1, 2, 4, 6 and 8 CTAs (us, bf16): 8 x 2048 x 1536 (192 columns) 41.4, 34.9, 38.3, 44.6, 47.3; 16 x 2048
+// x 1536: 55.7, 61.9, 69.0, 79.9, 88.4; 16 x 1024 x 1024: 24.1, 30.5, 31.2, 36.1, 41.3; 1 x 32768 x 5120:
+// 431, 321, 230, 249, 236; 4 x 8192 x 1536: 111, 87, 64, 77, 71; 3 was slower than its neighbours.
 constexpr int64_t kRecSlots = 3 * 148;
 
 int rec_cluster(int64_t columns, int64_t tiles)
