@@ -168,3 +168,34 @@ def test_explicit_capturing_stream_gpu(cuda_device):
             out.zero_()
             graph.replay()
             assert torch.equal(out, want)
+
+
+@pytest.mark.gpu
+def test_host_buffer_calls_on_streams_and_threads_gpu(cuda_device):
+    problems = [problem(30 + s, b=4, L=300 + 200 * s) for s in range(3)]
+    want = [scan.selective_scan_fwd(**p).cpu() for p in problems]
+    host = []
+    for p in problems:
+        q = {k: v for k, v in p.items() if k != "segments"}
+        q.update({k: p[k].cpu().pin_memory() for k in ("u", "delta", "B", "C")})
+        host.append(q)
+    streams = [torch.cuda.Stream() for _ in problems]
+    outs = [[torch.empty(w.shape, dtype=w.dtype, pin_memory=True) for _ in range(6)] for w in want]
+    torch.cuda.synchronize()
+
+    def work(i):
+        for r in range(6):
+            stream = streams[i] if r % 2 else streams[i].cuda_stream
+            scan.selective_scan_fwd_host(**host[i], out=outs[i][r], stream=stream, chunks=2)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        for v in o:
+            # pieces of whole rows, other segments: a rounding of the output apart
+            assert ((v.float() - w.float()).abs() <= 2.0 ** -7 * w.float().abs() + 1e-3).all()
+            assert torch.equal(v, o[0])
